@@ -102,10 +102,11 @@ extern "C" int fvattn_block_order(const fvattn_geom* g, int32_t* table, fvattn_s
 extern "C" int fvattn_get_status(fvattn_stream_t stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess) return FVATTN_ERR_CUDA;
-    // both words are read and cleared; the attention kernels' error is reported first
+    // every word is read and cleared; the attention kernels' error is reported first
     const int va = take_status_attn();
     const int vr = take_status_route();
-    return va != FVATTN_OK ? va : vr;
+    const int vg = take_status_grad();
+    return va != FVATTN_OK ? va : (vr != FVATTN_OK ? vr : vg);
 }
 
 extern "C" const char* fvattn_status_string(int code) {

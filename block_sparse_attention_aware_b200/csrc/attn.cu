@@ -48,6 +48,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "fvattn_train.h"
 #include "ptx.cuh"
 #include "sync.cuh"
 #include "tmap.cuh"
@@ -101,6 +102,7 @@ struct AttnArgs {
     int* counter;                // next item to hand out
     __nv_bfloat16* o;            // [B, H, Npad, D], or [B, N, H, D] when raster
     int raster;                  // write O rows straight to the raster layout (real tokens only)
+    float* lse;                  // [B, H, Npad] log-sum-exp of each row (LSE instances)
     unsigned long long* sm_stats;
     float scale_log2;            // scale * log2(e), > 0
     int total_items;
@@ -194,9 +196,24 @@ __device__ __forceinline__ int union_slot(const uint32_t* ul, int cl, int bpc, i
     return j;
 }
 
+// Chunks of 128 keys that an item of cnt kv blocks walks.  LSE instances
+// accept rows that keep no block (cnt = 0): such an item walks one chunk with
+// no block in it, whose key mask is empty, so its barriers turn as always and
+// its rows end with sum 0.
+template <bool LSE>
+__device__ __forceinline__ int item_chunks(int cnt, int bpc) {
+    const int nc = (cnt + bpc - 1) / bpc;
+    return LSE && nc == 0 ? 1 : nc;
+}
+
 // GRP: 128-row tiles of G = 128 / bs > 1 query blocks walking the union of
 // their kv lists (bs < 128); otherwise one query block per tile.
-template <int D, bool GRP>
+// LSE: each row's natural log-sum-exp of its scaled scores is written too,
+// (M + log2(l_0 2^(m_0-M) + l_1 2^(m_1-M))) / log2(e) from the merged (m, l)
+// that the epilogue has at hand: one 4-byte store a row.  -inf for a row that
+// keeps no block (O = 0).  A template parameter, so the instances without it
+// stay as they are.
+template <int D, bool GRP, bool LSE = false>
 __global__ void __launch_bounds__(ATT_THREADS, 1)
     sparse_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
@@ -306,7 +323,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl.item_empty[slot]));
             if (!valid) break;
-            const int nc = (cnt + bpc - 1) / bpc;
+            const int nc = item_chunks<LSE>(cnt, bpc);
             float m_ref = -INFINITY;   // reference maximum, log2 units
             float l = 0.f;
             bool mine_any = false;
@@ -522,6 +539,12 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                 orow = a.o + ((static_cast<long long>(bh) * g.Npad) + static_cast<long long>(qb) * bs + row) * D;
                 store = in_tile;
             }
+            if constexpr (LSE) {
+                const float lsum = __fadd_rn(__fmul_rn(l0, a0), __fmul_rn(l1, a1));
+                if (w == 0 && in_tile)
+                    a.lse[static_cast<long long>(bh) * g.Npad + static_cast<long long>(qb) * bs + row] =
+                        lsum == 0.f ? -INFINITY : (mm + log2f(lsum)) * 0.69314718055994531f;
+            }
             // this group writes output columns [w*D/2, w*D/2 + D/2)
 #pragma unroll 1
             for (int q = 0; q < D / 64; ++q) {
@@ -610,9 +633,10 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                 const int nq = min(G, g.nb - qb);         // query blocks in the tile
                 int cnt = GRP ? __ldg(a.gcnt + static_cast<long long>(bh) * a.ngroups + u)
                               : __ldg(a.kv_cnt + static_cast<long long>(bh) * g.nb + qb);
-                if (cnt < 1 || cnt > g.nb) {
+                constexpr int min_cnt = LSE ? 0 : 1;
+                if (cnt < min_cnt || cnt > g.nb) {
                     if (lane == 0) record_status(FVATTN_ERR_BOUNDS);
-                    cnt = cnt < 1 ? 1 : g.nb;
+                    cnt = cnt < min_cnt ? min_cnt : g.nb;
                 }
                 if (lane == 0) {
                     ctl.item[slot][0] = bh;
@@ -634,7 +658,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                 }
                 const int32_t* list = a.kv_idx + (static_cast<long long>(bh) * g.nb + qb) * g.nb;
                 const uint32_t* ul = GRP ? a.ulist + (static_cast<long long>(bh) * a.ngroups + u) * g.nb : nullptr;
-                const int nc = (cnt + bpc - 1) / bpc;
+                const int nc = item_chunks<LSE>(cnt, bpc);
                 // chunk cl's blocks (lane s < nblk: slot s), membership bits and real extents, one chunk
                 // ahead (the extent load is in flight while the current chunk is handled)
                 int j_next = 0;
@@ -744,7 +768,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                 const int G = GRP ? a.G : 1;
                 const int32_t* list = a.kv_idx + (static_cast<long long>(bh) * g.nb + qb) * g.nb;
                 const uint32_t* ul = GRP ? a.ulist + (static_cast<long long>(bh) * a.ngroups + qb / G) * g.nb : nullptr;
-                const int nc = (cnt + bpc - 1) / bpc;
+                const int nc = item_chunks<LSE>(cnt, bpc);
                 uint32_t m_unused = 0u;
                 int n_next = min(bpc, cnt);
                 int j_next = GRP ? union_slot(ul, 0, bpc, n_next, lane, g.nb, m_unused)
@@ -804,7 +828,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                     const int cnt = ctl.item[slot][2];
                     mbar_arrive(smem_u32(&ctl.item_empty[slot]));
                     if (!valid) break;
-                    const int nc = (cnt + bpc - 1) / bpc;
+                    const int nc = item_chunks<LSE>(cnt, bpc);
                     if (qk_role) {
                         blocks += static_cast<unsigned long long>(cnt);
                         if (!wait_bar(smem_u32(&ctl.q_full), item_seq & 1, abort_flag, wlim)) break;
@@ -890,8 +914,9 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
 // group's G kv lists in ascending block order, each entry the block id with
 // its membership bits (bit t: the block is in query block t's list) above
 // bit 24, and the union's size, which is the number of kv blocks the group's
-// tile walks.  Order and repeats inside a list do not matter.
-__global__ void __launch_bounds__(256) group_union_kernel(Geo g, int G, int ngroups, int nwords,
+// tile walks.  Order and repeats inside a list do not matter.  min_cnt: the
+// least list length that is in range.
+__global__ void __launch_bounds__(256) group_union_kernel(Geo g, int G, int ngroups, int nwords, int min_cnt,
                                                           const int32_t* __restrict__ kv_idx,
                                                           const int32_t* __restrict__ kv_cnt,
                                                           uint32_t* __restrict__ ulist, int32_t* __restrict__ gcnt) {
@@ -909,9 +934,9 @@ __global__ void __launch_bounds__(256) group_union_kernel(Geo g, int G, int ngro
         const int qb = grp * G + t;
         if (qb >= nb) break;
         int cnt = kv_cnt[bh * nb + qb];
-        if (cnt < 1 || cnt > nb) {
+        if (cnt < min_cnt || cnt > nb) {
             if (lane == 0) record_status(FVATTN_ERR_BOUNDS);
-            cnt = cnt < 1 ? 1 : nb;
+            cnt = cnt < min_cnt ? min_cnt : nb;
         }
         const int32_t* list = kv_idx + (bh * nb + qb) * nb;
         for (int e = lane; e < cnt; e += 32) {
@@ -1065,20 +1090,20 @@ static int cached_num_sms() {
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <int D, bool GRP>
+template <int D, bool GRP, bool LSE>
 static int launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& args,
                        int grid, cudaStream_t s) {
     using L = Smem<D>;
-    if (cudaFuncSetAttribute(sparse_attn_kernel<D, GRP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(sparse_attn_kernel<D, GRP, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(L::ALLOC)) != cudaSuccess)
         return FVATTN_ERR_CUDA;
     // The warpgroups' register shares (setmaxnreg) must fit in what a CTA is
     // launched with, or the raising warpgroups would wait for ever.
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, sparse_attn_kernel<D, GRP>) != cudaSuccess) return FVATTN_ERR_CUDA;
+    if (cudaFuncGetAttributes(&fa, sparse_attn_kernel<D, GRP, LSE>) != cudaSuccess) return FVATTN_ERR_CUDA;
     if (static_cast<long long>(fa.numRegs) * ATT_THREADS < 128ll * RegSplit<GRP>::LOW + 256ll * RegSplit<GRP>::HIGH)
         return FVATTN_ERR_UNSUPPORTED;
-    sparse_attn_kernel<D, GRP><<<grid, ATT_THREADS, L::ALLOC, s>>>(tq, tk, tv, args);
+    sparse_attn_kernel<D, GRP, LSE><<<grid, ATT_THREADS, L::ALLOC, s>>>(tq, tk, tv, args);
     FV_CHECK_LAUNCH();
     return FVATTN_OK;
 }
@@ -1102,7 +1127,8 @@ extern "C" int fvattn_test_hook(unsigned long long wait_limit_ns, int flags) {
 }
 
 static int attn_impl(const fvattn_geom* gp, const void* q_t, const void* k_t, const void* v_t, const int32_t* kv_idx,
-                     const int32_t* kv_cnt, float scale, void* o_t, int raster, unsigned long long* sm_stats,
+                     const int32_t* kv_cnt, float scale, void* o_t, int raster, float* lse,
+                     unsigned long long* sm_stats,
                      void* workspace, size_t ws_bytes, fvattn_stream_t stream) {
     if (!gp || !q_t || !k_t || !v_t || !kv_idx || !kv_cnt || !o_t || !workspace) return FVATTN_ERR_INVALID;
     if (!aligned16(q_t) || !aligned16(k_t) || !aligned16(v_t) || !aligned16(o_t) || !aligned16(kv_idx) ||
@@ -1131,7 +1157,7 @@ static int attn_impl(const fvattn_geom* gp, const void* q_t, const void* k_t, co
     if (wl.G > 1) {
         const long long warps = static_cast<long long>(BH) * wl.ngroups;
         group_union_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, sizeof(uint32_t) * 8 * wl.G * wl.nwords, s>>>(
-            g, wl.G, wl.ngroups, wl.nwords, kv_idx, kv_cnt, ulist, gcnt);
+            g, wl.G, wl.ngroups, wl.nwords, lse ? 0 : 1, kv_idx, kv_cnt, ulist, gcnt);
         FV_CHECK_LAUNCH();
     }
     worklist_head_kernel<<<BH, 256, sizeof(int) * (g.nb + 2), s>>>(g, units, wl.G > 1 ? gcnt : kv_cnt, item_order,
@@ -1154,6 +1180,7 @@ static int attn_impl(const fvattn_geom* gp, const void* q_t, const void* k_t, co
     args.counter = counter;
     args.o = static_cast<__nv_bfloat16*>(o_t);
     args.raster = raster;
+    args.lse = lse;
     args.sm_stats = sm_stats;
     args.scale_log2 = scale * 1.4426950408889634f;
     args.G = wl.G;
@@ -1168,25 +1195,40 @@ static int attn_impl(const fvattn_geom* gp, const void* q_t, const void* k_t, co
     int nsm = cached_num_sms();
     if (nsm <= 0) return FVATTN_ERR_CUDA;
     const int grid = nsm;
+    if (lse) {
+        if (wl.G > 1)
+            return g.D == 128 ? launch_attn<128, true, true>(tq, tk, tv, args, grid, s)
+                              : launch_attn<64, true, true>(tq, tk, tv, args, grid, s);
+        return g.D == 128 ? launch_attn<128, false, true>(tq, tk, tv, args, grid, s)
+                          : launch_attn<64, false, true>(tq, tk, tv, args, grid, s);
+    }
     if (wl.G > 1)
-        return g.D == 128 ? launch_attn<128, true>(tq, tk, tv, args, grid, s)
-                          : launch_attn<64, true>(tq, tk, tv, args, grid, s);
-    return g.D == 128 ? launch_attn<128, false>(tq, tk, tv, args, grid, s)
-                      : launch_attn<64, false>(tq, tk, tv, args, grid, s);
+        return g.D == 128 ? launch_attn<128, true, false>(tq, tk, tv, args, grid, s)
+                          : launch_attn<64, true, false>(tq, tk, tv, args, grid, s);
+    return g.D == 128 ? launch_attn<128, false, false>(tq, tk, tv, args, grid, s)
+                      : launch_attn<64, false, false>(tq, tk, tv, args, grid, s);
 }
 
 extern "C" int fvattn_sparse_attn(const fvattn_geom* gp, const void* q_t, const void* k_t, const void* v_t,
                                   const int32_t* kv_idx, const int32_t* kv_cnt, float scale, void* o_t,
                                   unsigned long long* sm_stats, void* workspace, size_t ws_bytes,
                                   fvattn_stream_t stream) {
-    return attn_impl(gp, q_t, k_t, v_t, kv_idx, kv_cnt, scale, o_t, 0, sm_stats, workspace, ws_bytes, stream);
+    return attn_impl(gp, q_t, k_t, v_t, kv_idx, kv_cnt, scale, o_t, 0, nullptr, sm_stats, workspace, ws_bytes, stream);
 }
 
 extern "C" int fvattn_sparse_attn_raster(const fvattn_geom* gp, const void* q_t, const void* k_t, const void* v_t,
                                          const int32_t* kv_idx, const int32_t* kv_cnt, float scale, void* o,
                                          unsigned long long* sm_stats, void* workspace, size_t ws_bytes,
                                          fvattn_stream_t stream) {
-    return attn_impl(gp, q_t, k_t, v_t, kv_idx, kv_cnt, scale, o, 1, sm_stats, workspace, ws_bytes, stream);
+    return attn_impl(gp, q_t, k_t, v_t, kv_idx, kv_cnt, scale, o, 1, nullptr, sm_stats, workspace, ws_bytes, stream);
+}
+
+extern "C" int fvattn_sparse_attn_lse(const fvattn_geom* gp, const void* q_t, const void* k_t, const void* v_t,
+                                      const int32_t* kv_idx, const int32_t* kv_cnt, float scale, void* o_t, float* lse,
+                                      unsigned long long* sm_stats, void* workspace, size_t ws_bytes,
+                                      fvattn_stream_t stream) {
+    if (!lse || !aligned16(lse)) return FVATTN_ERR_INVALID;
+    return attn_impl(gp, q_t, k_t, v_t, kv_idx, kv_cnt, scale, o_t, 0, lse, sm_stats, workspace, ws_bytes, stream);
 }
 
 int fv::take_status_attn() { return fv::take_tu_status(); }

@@ -52,6 +52,7 @@ static inline int take_tu_status() {
 // The status words of the files whose kernels record errors.
 int take_status_route();
 int take_status_attn();
+int take_status_grad();
 
 // Raster tile index of a block, and block of a raster tile (identities in
 // raster tile order).

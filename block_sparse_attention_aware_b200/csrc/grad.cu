@@ -1,0 +1,987 @@
+// Backward pass of the block-sparse attention (attn.cu): dQ, dK, dV from
+// Q, K, V, O, dO and the forward's log-sum-exp.
+//
+// Mathematics, per (b, h), on the kept real (query t, key u) pairs:
+//   P = exp2(scale log2e S - lse2),  S = Q K^T           (computed again)
+//   dP = dO V^T,  dS = P (dP - delta),  delta_t = dO_t . O_t
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
+//
+// Two passes over the pairs, one that keeps a key tile in place and sums dK
+// and dV over the query blocks that keep it, one that keeps a query tile in
+// place and sums dQ over its kept key blocks.  S and dP are formed in both:
+// seven products where five would do if dQ were added up in memory by
+// atomics, whose order would change the result's bits, or if dS were stored
+// (32 KB a pair of blocks).  Every sum here runs in one CTA in list order.
+//
+// Both passes are one kernel, grad_kernel<D, KV>, one CTA of 384 threads per
+// SM (it holds all 512 tensor-memory columns):
+//   warp 0      producer: takes items, TMA-loads the item's own tile pair
+//               (KV: K and V; else Q and dO), streams the first tensor of the
+//               other side (KV: Q; else K) in chunks of 128 rows and writes
+//               each chunk's mask words
+//   warp 2      producer of the other streamed tensor (KV: dO; else V)
+//   warp 1      one lane issues every MMA
+//   warps 4..11 two groups of four warps; a thread has one row of the
+//               128-row tile and half of the chunk's 128 columns: P and dS
+//               are formed from the fp32 S and dP in tensor memory and go
+//               back there as bf16, where they are the A operand of the
+//               accumulating products
+// KV: rows are keys, columns queries (S^T, dP^T); columns' statistics come
+// with the stream.  Else rows are queries with their statistics in registers.
+//
+// bs < 128: as in the forward, a tile holds G = 128 / bs consecutive blocks
+// and walks the union of their lists; a chunk packs 128 / bs listed blocks and
+// each row sees only the columns of blocks that its own block is paired with.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "fvattn_train.h"
+#include "ptx.cuh"
+#include "sync.cuh"
+#include "tmap.cuh"
+
+namespace fv {
+
+constexpr int GRAD_THREADS = 384;
+constexpr int GRAD_STAGES = 2;
+constexpr uint32_t GRAD_TMEM = 512;
+constexpr int GRAD_GROUP = 8;     // blocks per tile at bs = 16
+// Register split (setmaxnreg): the launch gives 168 a thread; one warpgroup
+// of producers and issuer at LOW, two of arithmetic at HIGH.
+constexpr int GRAD_LAUNCH_REGS = 168, GRAD_LOW = 72, GRAD_HIGH = 216;
+static_assert(128 * GRAD_LOW + 256 * GRAD_HIGH <= GRAD_THREADS * GRAD_LAUNCH_REGS, "register split");
+
+// Tensor-memory columns.  KV: S^T (P^T over it), dP^T (dS^T over it), dV, dK.
+// Else: two S buffers (dS over them), dP, dQ.
+constexpr uint32_t T_S = 0, T_DP_KV = 128, T_DV = 256, T_DK = 384;
+constexpr uint32_t T_DP_Q = 256, T_DQ = 384;
+
+struct GradArgs {
+    Geo g;
+    int G, ngroups;
+    const uint32_t* ul;       // [B*H][ngroups][nb] this pass's lists: block | membership bits << 24
+    const int32_t* cnt;       // [B*H][ngroups] their lengths
+    const int32_t* order;     // [B*H][ngroups] tiles of a head, longest first
+    int* counter;
+    const int32_t* ext;       // [nb] real extent of each block
+    const float* nlse2;       // [B*H][Npad] -lse * log2(e); -inf for rows that take no part
+    const float* ndelta;      // [B*H][Npad] -dO . O
+    __nv_bfloat16* out0;      // KV: dV; else dQ
+    __nv_bfloat16* out1;      // KV: dK
+    float scale, scale_log2;
+    int total_items;
+    int oob_row;              // a row index past the end of every operand (reads as zero)
+    unsigned long long wait_limit_ns;
+};
+
+struct __align__(16) GradCtrl {
+    float nlse2[GRAD_STAGES][128], ndelta[GRAD_STAGES][128];   // KV: the chunk's column statistics
+    uint32_t mask[GRAD_STAGES][GRAD_GROUP][4];                 // per block of the tile: columns its rows see
+    unsigned long long a_full, a_empty;                        // the item's own tile pair
+    unsigned long long b0_full[GRAD_STAGES], b0_empty[GRAD_STAGES];
+    unsigned long long b1_full[GRAD_STAGES], b1_empty[GRAD_STAGES];
+    unsigned long long s_full[2], dp_full, dp_free, p_full, ds_full[2];
+    unsigned long long acc_full, acc_free;
+    unsigned long long item_full[2], item_empty[2];
+    unsigned long long drain;
+    int item[2][4];            // bh, tile, list length, valid
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <int D>
+struct GradSmem {
+    static constexpr uint32_t TILE = 128u * D * 2u;
+    static constexpr uint32_t A0 = 0, A1 = TILE, B0 = 2 * TILE, B1 = B0 + GRAD_STAGES * TILE;
+    static constexpr uint32_t CTRL = B1 + GRAD_STAGES * TILE;
+    static constexpr uint32_t TOTAL = CTRL + static_cast<uint32_t>(sizeof(GradCtrl));
+    // at least 120 KB, so that two CTAs never share an SM's tensor memory
+    static constexpr uint32_t ALLOC = TOTAL > 120u * 1024u ? TOTAL : 120u * 1024u;
+    static_assert(ALLOC <= 232448u, "shared-memory layout too large");
+};
+
+// Real extent of a block, packed nf | ny << 8 | nx << 16.
+__device__ __forceinline__ int grad_extent(const Geo& g, int block) {
+    block = tile_of_block(g, block);
+    const int bx = block % g.nbx;
+    const int rest = block / g.nbx;
+    const int by = rest % g.nby;
+    const int bf = rest / g.nby;
+    return min(g.tf, g.F - bf * g.tf) | (min(g.th, g.Hs - by * g.th) << 8) | (min(g.tw, g.Ws - bx * g.tw) << 16);
+}
+
+// One slot of a chunk: its block (-1: none) and membership bits.
+__device__ __forceinline__ int grad_slot(const uint32_t* ul, int e, int cnt, uint32_t& mem) {
+    mem = 0u;
+    if (e >= cnt) return -1;
+    const uint32_t v = __ldg(ul + e);
+    mem = v >> 24;
+    return static_cast<int>(v & 0xFFFFFFu);
+}
+
+template <int D, bool KV>
+__global__ void __launch_bounds__(GRAD_THREADS, 1)
+    grad_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
+                const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, const GradArgs a) {
+    using L = GradSmem<D>;
+    constexpr int NS = GRAD_STAGES;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    if (smem_u32(smem) & 1023u) {   // the 128-byte swizzle needs 1024-byte aligned tiles
+        if (threadIdx.x == 0) record_status(FVATTN_ERR_UNSUPPORTED);
+        return;
+    }
+    GradCtrl& ctl = *reinterpret_cast<GradCtrl*>(smem + L::CTRL);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const Geo& g = a.g;
+    const int bs = g.bs;
+    const int bpc = 128 / bs;
+    volatile int* abort_flag = &ctl.abort_flag;
+    const unsigned long long wlim = a.wait_limit_ns;
+
+    {   // rows that no load of the first item fills must be finite
+        uint4* z = reinterpret_cast<uint4*>(smem);
+        for (uint32_t i = threadIdx.x; i < L::CTRL / 16u; i += GRAD_THREADS) z[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&ctl.a_full), 1);
+        mbar_init(smem_u32(&ctl.a_empty), 1);
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(smem_u32(&ctl.b0_full[s]), 1);
+            mbar_init(smem_u32(&ctl.b0_empty[s]), 1 + 8);   // the MMAs' commit and the eight arithmetic warps
+            mbar_init(smem_u32(&ctl.b1_full[s]), 1);
+            mbar_init(smem_u32(&ctl.b1_empty[s]), KV ? 1 + 8 : 1);
+            mbar_init(smem_u32(&ctl.s_full[s]), 1);
+            mbar_init(smem_u32(&ctl.ds_full[s]), 8);
+            mbar_init(smem_u32(&ctl.item_full[s]), 1);
+            mbar_init(smem_u32(&ctl.item_empty[s]), 1 + 1 + 8);   // issuer, second producer, arithmetic
+        }
+        mbar_init(smem_u32(&ctl.dp_full), 1);
+        mbar_init(smem_u32(&ctl.dp_free), 8);
+        mbar_init(smem_u32(&ctl.p_full), 8);
+        mbar_init(smem_u32(&ctl.acc_full), 1);
+        mbar_init(smem_u32(&ctl.acc_free), 8);
+        mbar_init(smem_u32(&ctl.drain), 1);
+        ctl.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tmA0);
+        prefetch_tmap(&tmA1);
+        prefetch_tmap(&tmB0);
+        prefetch_tmap(&tmB1);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&ctl.tmem_base), GRAD_TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem_base;
+
+    if (warp >= 4) {
+        regs_inc<GRAD_HIGH>();
+        // =========================== arithmetic: P, dS, epilogue
+        const int w = (warp - 4) >> 2;              // columns 64 w ..
+        const int quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const int tb = row / bs;                    // this row's block in the tile
+        const unsigned long long sl2x2 = f2_pack(a.scale_log2, a.scale_log2);
+        int item_seq = 0;
+        uint32_t n_seq = 0;     // items with at least one chunk
+        uint32_t c = 0;         // chunks
+        bool ok = true;
+        while (ok) {
+            const int slot = item_seq & 1;
+            if (!wait_warp(smem_u32(&ctl.item_full[slot]), (item_seq >> 1) & 1, abort_flag, wlim)) break;
+            const int bh = ctl.item[slot][0];
+            const int u = ctl.item[slot][1];
+            const int cnt = ctl.item[slot][2];
+            const int valid = ctl.item[slot][3];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.item_empty[slot]));
+            if (!valid) break;
+            const int nc = (cnt + bpc - 1) / bpc;
+            const int blk0 = u * a.G;
+            const bool in_tile = row < min(a.G, g.nb - blk0) * bs;
+            const long long grow = static_cast<long long>(bh) * g.Npad + static_cast<long long>(blk0) * bs + row;
+            // KV: whether this key row is a token.  Else: the query row's statistics (-inf takes P to 0).
+            uint32_t row_mask = 0xFFFFFFFFu;
+            unsigned long long nl2 = 0ull, nd2 = 0ull;
+            if (KV) {
+                int f_, y_, x_;
+                if (!in_tile || !token_of_pos(g, static_cast<long long>(blk0) * bs + row, f_, y_, x_)) row_mask = 0u;
+            } else {
+                const float nl = in_tile ? __ldg(a.nlse2 + grow) : -INFINITY;
+                const float nd = in_tile ? __ldg(a.ndelta + grow) : 0.f;
+                nl2 = f2_pack(nl, nl);
+                nd2 = f2_pack(nd, nd);
+                if (nl == -INFINITY) row_mask = 0u;
+            }
+            for (int i = 0; i < nc; ++i, ++c) {
+                const int st = c % NS;
+                const uint32_t sbuf = trow + T_S + (KV ? 0u : (c & 1u) * 128u) + static_cast<uint32_t>(w) * 64u;
+                const uint32_t dpbuf = trow + (KV ? T_DP_KV : T_DP_Q) + static_cast<uint32_t>(w) * 64u;
+                const uint32_t sbar = KV ? smem_u32(&ctl.s_full[0]) : smem_u32(&ctl.s_full[c & 1]);
+                const uint32_t spar = KV ? (c & 1) : ((c >> 1) & 1);
+                if (!wait_warp2(smem_u32(&ctl.b0_full[st]), (c / NS) & 1, sbar, spar, abort_flag, wlim)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t mw[2];
+                mw[0] = ctl.mask[st][tb][2 * w] & row_mask;
+                mw[1] = ctl.mask[st][tb][2 * w + 1] & row_mask;
+                float p[2][32];
+                {
+                    uint32_t s0[32], s1[32];
+                    tmem_ld32(sbuf, s0);
+                    tmem_ld32(sbuf + 32u, s1);
+                    tmem_wait_ld();
+                    auto probs = [&](int h, const uint32_t (&sv)[32]) {
+                        if (mw[h] == 0u) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) p[h][e] = 0.f;
+                            return;
+                        }
+                        const unsigned long long* nls =
+                            reinterpret_cast<const unsigned long long*>(&ctl.nlse2[st][w * 64 + h * 32]);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const unsigned long long add = KV ? nls[e >> 1] : nl2;
+                            float x0, x1;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2x2, add),
+                                      x0, x1);
+                            p[h][e] = ex2_approx(x0);
+                            p[h][e + 1] = ex2_approx(x1);
+                        }
+                        if (mw[h] != 0xFFFFFFFFu) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) p[h][e] = ((mw[h] >> e) & 1u) ? p[h][e] : 0.f;
+                        }
+                    };
+                    probs(0, s0);
+                    probs(1, s1);
+                }
+                if (KV) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(p[e >> 4][(2 * e) & 31], p[e >> 4][(2 * e + 1) & 31]);
+                    tmem_st32(sbuf, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&ctl.p_full));
+                        mbar_arrive(smem_u32(&ctl.b0_empty[st]));
+                    }
+                    if (!wait_warp2(smem_u32(&ctl.b1_full[st]), (c / NS) & 1, smem_u32(&ctl.dp_full), c & 1, abort_flag,
+                                    wlim)) {
+                        ok = false;
+                        break;
+                    }
+                } else {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&ctl.b0_empty[st]));
+                    if (!wait_warp(smem_u32(&ctl.dp_full), c & 1, abort_flag, wlim)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                tc_fence_after();
+                {
+                    uint32_t d0[32], d1[32], ds[32];
+                    tmem_ld32(dpbuf, d0);
+                    tmem_ld32(dpbuf + 32u, d1);
+                    tmem_wait_ld();
+                    if (!KV) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&ctl.dp_free));
+                    }
+                    auto grads = [&](int h, const uint32_t (&dv)[32]) {
+                        const unsigned long long* nds =
+                            reinterpret_cast<const unsigned long long*>(&ctl.ndelta[st][w * 64 + h * 32]);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const unsigned long long add = KV ? nds[e >> 1] : nd2;
+                            float x0, x1;
+                            f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), add),
+                                             f2_pack(p[h][e], p[h][e + 1])), x0, x1);
+                            // a masked pair gives 0 whatever dP holds
+                            if (mw[h] != 0xFFFFFFFFu) {
+                                x0 = ((mw[h] >> e) & 1u) ? x0 : 0.f;
+                                x1 = ((mw[h] >> (e + 1)) & 1u) ? x1 : 0.f;
+                            }
+                            ds[h * 16 + (e >> 1)] = pack_bf16x2(x0, x1);
+                        }
+                    };
+                    grads(0, d0);
+                    grads(1, d1);
+                    tmem_st32(KV ? dpbuf : sbuf, ds);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&ctl.ds_full[c & 1]));
+                        if (KV) mbar_arrive(smem_u32(&ctl.b1_empty[st]));
+                    }
+                }
+            }
+            if (!ok) break;
+            // ---- epilogue.  KV: group 0 writes dV, group 1 dK; else each writes half of dQ's columns.
+            if (nc > 0) {
+                if (!wait_warp(smem_u32(&ctl.acc_full), n_seq & 1, abort_flag, wlim)) break;
+                tc_fence_after();
+            }
+            const float f = KV ? (w == 0 ? 1.f : a.scale) : a.scale;
+            __nv_bfloat16* dst = (KV && w == 1 ? a.out1 : a.out0) + grow * D;
+            const uint32_t acc = trow + (KV ? (w == 0 ? T_DV : T_DK) : T_DQ);
+            constexpr int NQ = KV ? D / 32 : D / 64;
+#pragma unroll 1
+            for (int q = 0; q < NQ; ++q) {
+                const uint32_t col = (KV ? 0u : static_cast<uint32_t>(w) * (D / 2)) + q * 32u;
+                uint32_t r[32];
+                if (nc > 0) {
+                    tmem_ld32(acc + col, r);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = 0u;
+                }
+                if (in_tile) {
+#pragma unroll
+                    for (int v8 = 0; v8 < 4; ++v8) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            o[k] = pack_bf16x2(__uint_as_float(r[v8 * 8 + 2 * k]) * f,
+                                               __uint_as_float(r[v8 * 8 + 2 * k + 1]) * f);
+                        *reinterpret_cast<uint4*>(dst + col + v8 * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+            if (nc > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl.acc_free));
+                ++n_seq;
+            }
+            ++item_seq;
+        }
+    } else {
+        regs_dec<GRAD_LOW>();
+        if (warp == 0) {
+            // =========================== producer: items, own tiles, first streamed tensor, masks
+            int c_slot[4], c_of[4], c_oy[4], c_ox[4];   // column q*32 + lane of a chunk
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int col = q * 32 + lane;
+                c_slot[q] = col / bs;
+                const int off = col - c_slot[q] * bs;
+                c_ox[q] = off % g.tw;
+                c_oy[q] = (off / g.tw) % g.th;
+                c_of[q] = off / (g.tw * g.th);
+            }
+            int item_seq = 0;
+            uint32_t n_seq = 0, c = 0;
+            bool ok = true;
+            while (ok) {
+                const int slot = item_seq & 1;
+                if (!wait_warp(smem_u32(&ctl.item_empty[slot]), ((item_seq >> 1) & 1) ^ 1, abort_flag, wlim)) break;
+                int t = 0;
+                if (lane == 0) t = atomicAdd(a.counter, 1);
+                t = __shfl_sync(0xffffffffu, t, 0);
+                if (t >= a.total_items) {
+                    if (lane == 0) {
+                        ctl.item[slot][3] = 0;
+                        mbar_arrive(smem_u32(&ctl.item_full[slot]));
+                    }
+                    break;
+                }
+                const int bh = t / a.ngroups;
+                const int u = __ldg(a.order + t);
+                const long long unit = static_cast<long long>(bh) * a.ngroups + u;
+                const int cnt = __ldg(a.cnt + unit);
+                if (lane == 0) {
+                    ctl.item[slot][0] = bh;
+                    ctl.item[slot][1] = u;
+                    ctl.item[slot][2] = cnt;
+                    ctl.item[slot][3] = 1;
+                    mbar_arrive(smem_u32(&ctl.item_full[slot]));
+                }
+                ++item_seq;
+                const int nc = (cnt + bpc - 1) / bpc;
+                if (nc == 0) continue;
+                const int blk0 = u * a.G;
+                const int nq = min(a.G, g.nb - blk0);
+                const int row_base = bh * static_cast<int>(g.Npad);
+                if (!wait_warp(smem_u32(&ctl.a_empty), (n_seq & 1) ^ 1, abort_flag, wlim)) break;
+                ++n_seq;
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&ctl.a_full), static_cast<uint32_t>(2 * nq * bs * D * 2));
+                __syncwarp();
+                if (lane < nq) {
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h) {
+                        const uint32_t off = h * 16384u + static_cast<uint32_t>(lane * bs) * 128u;
+                        tma_load_2d(sbase + L::A0 + off, &tmA0, h * 64, row_base + (blk0 + lane) * bs, smem_u32(&ctl.a_full));
+                        tma_load_2d(sbase + L::A1 + off, &tmA1, h * 64, row_base + (blk0 + lane) * bs, smem_u32(&ctl.a_full));
+                    }
+                }
+                const uint32_t* ul = a.ul + unit * g.nb;
+                for (int i = 0; i < nc; ++i, ++c) {
+                    const int st = c % NS;
+                    uint32_t mem = 0u;
+                    const int j = lane < bpc ? grad_slot(ul, i * bpc + lane, cnt, mem) : -1;
+                    const int ext = !KV && j >= 0 ? __ldg(a.ext + j) : 0;
+                    if (!wait_warp(smem_u32(&ctl.b0_empty[st]), ((c / NS) & 1) ^ 1, abort_flag, wlim)) {
+                        ok = false;
+                        break;
+                    }
+                    // columns a row of the tile's block tq sees: the slot's block is paired with tq, and
+                    // (for keys) the column is a token.  Query rows take no part through their statistics.
+                    uint32_t pad[4], mq[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int e = __shfl_sync(0xffffffffu, ext, c_slot[q]);
+                        mq[q] = __shfl_sync(0xffffffffu, mem, c_slot[q]);
+                        pad[q] = KV ? 0xFFFFFFFFu
+                                    : __ballot_sync(0xffffffffu, (c_of[q] < (e & 255)) && (c_oy[q] < ((e >> 8) & 255)) &&
+                                                                     (c_ox[q] < (e >> 16)));
+                    }
+                    for (int tq = 0; tq < a.G; ++tq) {
+                        uint32_t words[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) words[q] = pad[q] & __ballot_sync(0xffffffffu, (mq[q] >> tq) & 1u);
+                        if (lane == 0) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) ctl.mask[st][tq][q] = words[q];
+                        }
+                    }
+                    const uint32_t bar = smem_u32(&ctl.b0_full[st]);
+                    const int nblk = min(bpc, cnt - i * bpc);
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(bar, L::TILE + (KV ? static_cast<uint32_t>(nblk * bs * 4) : 0u));
+                    __syncwarp();
+                    if (lane < bpc) {
+                        // a slot without a block is filled with zeros (a row past the end): P is 0 there, and
+                        // 0 times what an earlier chunk left could be NaN
+                        const int r = j >= 0 ? row_base + j * bs : a.oob_row;
+                        const uint32_t dst = sbase + L::B0 + st * L::TILE + static_cast<uint32_t>(lane * bs) * 128u;
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + h * 16384u, &tmB0, h * 64, r, bar);
+                        if (KV && j >= 0)
+                            bulk_load(smem_u32(&ctl.nlse2[st][lane * bs]), a.nlse2 + r, static_cast<uint32_t>(bs * 4), bar);
+                    }
+                }
+            }
+            if (lane == 0) {   // no copy into shared memory outlives the CTA
+                if (n_seq > 0) wait_bar_drain(smem_u32(&ctl.a_full), (n_seq - 1) & 1, wlim);
+                for (int st = 0; st < NS; ++st) {
+                    const uint32_t fills = c > static_cast<uint32_t>(st) ? (c - st + NS - 1) / NS : 0u;
+                    if (fills > 0) wait_bar_drain(smem_u32(&ctl.b0_full[st]), (fills - 1) & 1, wlim);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // =========================== producer of the second streamed tensor
+            int item_seq = 0;
+            uint32_t c = 0;
+            bool ok = true;
+            while (ok) {
+                const int slot = item_seq & 1;
+                if (!wait_warp(smem_u32(&ctl.item_full[slot]), (item_seq >> 1) & 1, abort_flag, wlim)) break;
+                const int bh = ctl.item[slot][0];
+                const int u = ctl.item[slot][1];
+                const int cnt = ctl.item[slot][2];
+                const int valid = ctl.item[slot][3];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl.item_empty[slot]));
+                if (!valid) break;
+                ++item_seq;
+                const int nc = (cnt + bpc - 1) / bpc;
+                const int row_base = bh * static_cast<int>(g.Npad);
+                const uint32_t* ul = a.ul + (static_cast<long long>(bh) * a.ngroups + u) * g.nb;
+                for (int i = 0; i < nc; ++i, ++c) {
+                    const int st = c % NS;
+                    uint32_t mem = 0u;
+                    const int j = lane < bpc ? grad_slot(ul, i * bpc + lane, cnt, mem) : -1;
+                    if (!wait_warp(smem_u32(&ctl.b1_empty[st]), ((c / NS) & 1) ^ 1, abort_flag, wlim)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_u32(&ctl.b1_full[st]);
+                    const int nblk = min(bpc, cnt - i * bpc);
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(bar, L::TILE + (KV ? static_cast<uint32_t>(nblk * bs * 4) : 0u));
+                    __syncwarp();
+                    if (lane < bpc) {
+                        const int r = j >= 0 ? row_base + j * bs : a.oob_row;
+                        const uint32_t dst = sbase + L::B1 + st * L::TILE + static_cast<uint32_t>(lane * bs) * 128u;
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + h * 16384u, &tmB1, h * 64, r, bar);
+                        if (KV && j >= 0)
+                            bulk_load(smem_u32(&ctl.ndelta[st][lane * bs]), a.ndelta + r, static_cast<uint32_t>(bs * 4), bar);
+                    }
+                }
+            }
+            if (lane == 0) {
+                for (int st = 0; st < NS; ++st) {
+                    const uint32_t fills = c > static_cast<uint32_t>(st) ? (c - st + NS - 1) / NS : 0u;
+                    if (fills > 0) wait_bar_drain(smem_u32(&ctl.b1_full[st]), (fills - 1) & 1, wlim);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // =========================== MMA issuer (one lane)
+            if (lane == 0) {
+                constexpr uint32_t ID_SS = idesc_bf16_f32(128, 128, false);
+                constexpr uint32_t ID_ACC = idesc_bf16_f32(128, D, true);
+                // C = own tile (A, K-major) x streamed chunk (B, K-major)
+                auto product = [&](uint32_t d, uint32_t abase, uint32_t bbase) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * 16384u + (kk & 3) * 32u;
+                        mma_bf16_ss(d, sw128_desc(abase + off, 16u, 1024u), sw128_desc(bbase + off, 16u, 1024u), ID_SS,
+                                    kk > 0 ? 1u : 0u);
+                    }
+                };
+                // acc += A (bf16 in tensor memory, 64 columns of K in each of two 64-column halves) x chunk
+                // (B, its 128 rows are K)
+                auto accumulate = [&](uint32_t d, uint32_t abuf, uint32_t bbase, bool first) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_bf16_ts(d, abuf + (kk >> 2) * 64u + (kk & 3) * 8u, sw128_desc(bbase + kk * 2048u, 16384u, 1024u),
+                                    ID_ACC, (first && kk == 0) ? 0u : 1u);
+                };
+                const uint32_t sA0 = sbase + L::A0, sA1 = sbase + L::A1, sB0 = sbase + L::B0, sB1 = sbase + L::B1;
+                int item_seq = 0;
+                uint32_t n_seq = 0, c0 = 0;
+                bool ok = true;
+                auto need = [&](uint32_t bar, uint32_t parity) {
+                    if (ok) ok = wait_bar(bar, parity, abort_flag, wlim);
+                    return ok;
+                };
+                while (ok) {
+                    const int slot = item_seq & 1;
+                    if (!need(smem_u32(&ctl.item_full[slot]), (item_seq >> 1) & 1)) break;
+                    const int valid = ctl.item[slot][3];
+                    const int cnt = ctl.item[slot][2];
+                    mbar_arrive(smem_u32(&ctl.item_empty[slot]));
+                    if (!valid) break;
+                    ++item_seq;
+                    const int nc = (cnt + bpc - 1) / bpc;
+                    if (nc == 0) continue;
+                    if (!need(smem_u32(&ctl.a_full), n_seq & 1)) break;
+                    for (int i = 0; i <= nc; ++i) {
+                        const uint32_t c = c0 + i;
+                        const int st = c % NS;
+                        const uint32_t ph = (c / NS) & 1;
+                        if (i < nc) {
+                            // S: its buffer was last read by an accumulating product issued before
+                            if (!need(smem_u32(&ctl.b0_full[st]), ph)) break;
+                            tc_fence_after();
+                            product(tmem + T_S + (KV ? 0u : (c & 1u) * 128u), sA0, sB0 + st * L::TILE);
+                            mma_commit(smem_u32(&ctl.s_full[KV ? 0 : (c & 1)]));
+                        }
+                        if (KV) {
+                            if (i > 0) {   // dK += dS^T Q of the chunk before
+                                const int sp = (c - 1) % NS;
+                                if (!need(smem_u32(&ctl.ds_full[(c - 1) & 1]), ((c - 1) >> 1) & 1)) break;
+                                if (i == 1 && !need(smem_u32(&ctl.acc_free), (n_seq & 1) ^ 1)) break;
+                                tc_fence_after();
+                                accumulate(tmem + T_DK, tmem + T_DP_KV, sB0 + sp * L::TILE, i == 1);
+                                mma_commit(smem_u32(&ctl.b0_empty[sp]));
+                            }
+                            if (i < nc) {
+                                if (!need(smem_u32(&ctl.b1_full[st]), ph)) break;
+                                tc_fence_after();
+                                product(tmem + T_DP_KV, sA1, sB1 + st * L::TILE);
+                                mma_commit(smem_u32(&ctl.dp_full));
+                                if (i == nc - 1) mma_commit(smem_u32(&ctl.a_empty));
+                                if (!need(smem_u32(&ctl.p_full), c & 1)) break;
+                                if (i == 0 && !need(smem_u32(&ctl.acc_free), (n_seq & 1) ^ 1)) break;
+                                tc_fence_after();
+                                accumulate(tmem + T_DV, tmem + T_S, sB1 + st * L::TILE, i == 0);
+                                mma_commit(smem_u32(&ctl.b1_empty[st]));
+                            }
+                        } else {
+                            if (i < nc) {
+                                // dP: the arithmetic has read the chunk before's
+                                if (!need(smem_u32(&ctl.b1_full[st]), ph)) break;
+                                if (c > 0 && !need(smem_u32(&ctl.dp_free), (c - 1) & 1)) break;
+                                tc_fence_after();
+                                product(tmem + T_DP_Q, sA1, sB1 + st * L::TILE);
+                                mma_commit(smem_u32(&ctl.dp_full));
+                                mma_commit(smem_u32(&ctl.b1_empty[st]));
+                                if (i == nc - 1) mma_commit(smem_u32(&ctl.a_empty));
+                            }
+                            if (i > 0) {   // dQ += dS K of the chunk before
+                                const uint32_t cp = c - 1;
+                                const int sp = cp % NS;
+                                if (!need(smem_u32(&ctl.ds_full[cp & 1]), (cp >> 1) & 1)) break;
+                                if (i == 1 && !need(smem_u32(&ctl.acc_free), (n_seq & 1) ^ 1)) break;
+                                tc_fence_after();
+                                accumulate(tmem + T_DQ, tmem + T_S + (cp & 1u) * 128u, sB0 + sp * L::TILE, i == 1);
+                                mma_commit(smem_u32(&ctl.b0_empty[sp]));
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit(smem_u32(&ctl.acc_full));
+                    c0 += nc;
+                    ++n_seq;
+                }
+                // every MMA issued has completed before the tensor memory is released
+                mma_commit(smem_u32(&ctl.drain));
+                wait_bar_drain(smem_u32(&ctl.drain), 0, wlim);
+            }
+            __syncwarp();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, GRAD_TMEM);
+}
+
+// ------------------------------------------------------------------ statistics, lists, work order
+
+// First `stat_blocks` CTAs: -lse * log2(e) and -dO . O of every row (one warp
+// per 8 rows; 16 bytes of O and dO a lane), the former -inf for padding rows
+// and rows that keep no block, so that their P is 0.  The others: one warp
+// per (b, h, query block) writes its kv list as a bit row.
+template <int D>
+__global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, int nwords,
+                                                        const uint4* __restrict__ o, const uint4* __restrict__ dout,
+                                                        const float* __restrict__ lse,
+                                                        const int32_t* __restrict__ kv_idx,
+                                                        const int32_t* __restrict__ kv_cnt,
+                                                        float* __restrict__ nlse2, float* __restrict__ ndelta,
+                                                        uint32_t* __restrict__ bits) {
+    extern __shared__ uint32_t gp_bits[];   // [8][nwords]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (static_cast<int>(blockIdx.x) < stat_blocks) {
+        constexpr int LPR = D / 8;           // lanes a row
+        constexpr int RPI = 32 / LPR;        // rows an iteration
+        const long long rows = static_cast<long long>(g.B) * g.H * g.Npad;
+        const long long row0 = (static_cast<long long>(blockIdx.x) * 8 + warp) * 8;
+        if (row0 >= rows) return;
+        uint4 x[8 / RPI], y[8 / RPI];        // Npad is a multiple of 16: the 8 rows exist
+#pragma unroll
+        for (int i = 0; i < 8 / RPI; ++i) {
+            const long long at = (row0 + i * RPI) * LPR + lane;
+            x[i] = __ldg(o + at);
+            y[i] = __ldg(dout + at);
+        }
+#pragma unroll
+        for (int i = 0; i < 8 / RPI; ++i) {
+            const uint32_t xa[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ya[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s = fmaf(__uint_as_float(xa[k] << 16), __uint_as_float(ya[k] << 16), s);
+                s = fmaf(__uint_as_float(xa[k] & 0xFFFF0000u), __uint_as_float(ya[k] & 0xFFFF0000u), s);
+            }
+#pragma unroll
+            for (int d = LPR / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            if (lane % LPR == 0) ndelta[row0 + i * RPI + lane / LPR] = -s;
+        }
+        if (lane < 8) {
+            const long long r = row0 + lane;
+            int f_, y_, x_;
+            const float l = lse[r];
+            const bool takes_part = token_of_pos(g, r % g.Npad, f_, y_, x_) && l != -INFINITY;
+            nlse2[r] = takes_part ? -l * 1.4426950408889634f : -INFINITY;
+        }
+        return;
+    }
+    const long long unit = (static_cast<long long>(blockIdx.x) - stat_blocks) * 8 + warp;
+    if (unit >= static_cast<long long>(g.B) * g.H * g.nb) return;
+    uint32_t* mine = gp_bits + warp * nwords;
+    for (int i = lane; i < nwords; i += 32) mine[i] = 0u;
+    __syncwarp();
+    int cnt = __ldg(kv_cnt + unit);
+    if (cnt < 0 || cnt > g.nb) {
+        if (lane == 0) record_status(FVATTN_ERR_BOUNDS);
+        cnt = cnt < 0 ? 0 : g.nb;
+    }
+    const int32_t* list = kv_idx + unit * g.nb;
+    for (int e = lane; e < cnt; e += 32) {
+        const int j = __ldg(list + e);
+        if (j < 0 || j >= g.nb) {
+            record_status(FVATTN_ERR_BOUNDS);
+            continue;
+        }
+        if (atomicOr(&mine[j >> 5], 1u << (j & 31)) & (1u << (j & 31))) record_status(FVATTN_ERR_BOUNDS);
+    }
+    __syncwarp();
+    for (int i = lane; i < nwords; i += 32) bits[unit * nwords + i] = mine[i];
+}
+
+// One warp per (direction, b, h, tile): the blocks that a tile of G blocks is
+// paired with, ascending, each with its membership bits above bit 24 (bit t:
+// paired with the tile's block t).  Direction 0: a query tile and key blocks,
+// from the rows of the bit matrix; 1: a key tile and query blocks, from its
+// columns.
+__global__ void __launch_bounds__(256) grad_lists_kernel(Geo g, int G, int ngroups, int nwords,
+                                                         const uint32_t* __restrict__ bits,
+                                                         uint32_t* __restrict__ ulq, int32_t* __restrict__ cntq,
+                                                         uint32_t* __restrict__ ulk, int32_t* __restrict__ cntk) {
+    const int lane = threadIdx.x & 31;
+    const long long units = static_cast<long long>(g.B) * g.H * ngroups;
+    long long unit = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const bool keys = unit >= units;
+    if (keys) unit -= units;
+    if (unit >= units) return;
+    const long long bh = unit / ngroups;
+    const int u = static_cast<int>(unit - bh * ngroups);
+    const uint32_t* mat = bits + bh * g.nb * nwords;
+    int base = 0;
+    if (!keys) {
+        uint32_t* dst = ulq + unit * g.nb;
+        const int q0 = u * G, nq = min(G, g.nb - q0);
+        for (int w0 = 0; w0 < nwords; w0 += 32) {
+            const int wd = w0 + lane;
+            uint32_t row[GRAD_GROUP], un = 0u;
+#pragma unroll
+            for (int t = 0; t < GRAD_GROUP; ++t) {
+                row[t] = t < nq && wd < nwords ? __ldg(mat + static_cast<long long>(q0 + t) * nwords + wd) : 0u;
+                un |= row[t];
+            }
+            const int c = __popc(un);
+            int incl = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            int k = base + incl - c;
+            for (uint32_t r = un; r != 0u; r &= r - 1u) {
+                const int b = __ffs(static_cast<int>(r)) - 1;
+                uint32_t mem = 0u;
+#pragma unroll
+                for (int t = 0; t < GRAD_GROUP; ++t) mem |= ((row[t] >> b) & 1u) << t;
+                dst[k++] = static_cast<uint32_t>(wd * 32 + b) | (mem << 24);
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) cntq[unit] = base;
+    } else {
+        uint32_t* dst = ulk + unit * g.nb;
+        const int wd = (u * G) >> 5, sh = (u * G) & 31;   // G divides 32: one word holds the tile's columns
+        const uint32_t ones = (1u << G) - 1u;
+        for (int i0 = 0; i0 < g.nb; i0 += 32) {
+            const int i = i0 + lane;
+            const uint32_t mem = i < g.nb ? (__ldg(mat + static_cast<long long>(i) * nwords + wd) >> sh) & ones : 0u;
+            const uint32_t any = __ballot_sync(0xffffffffu, mem != 0u);
+            if (mem) dst[base + __popc(any & ((1u << lane) - 1u))] = static_cast<uint32_t>(i) | (mem << 24);
+            base += __popc(any);
+        }
+        if (lane == 0) cntk[unit] = base;
+    }
+}
+
+// One CTA per (direction, b, h): the head's tiles by list length, longest
+// first (a counting sort; which of two equal tiles comes first changes only
+// the schedule).  The first CTA of a direction resets its item counter.
+__global__ void __launch_bounds__(256) grad_order_kernel(int BH, int ngroups, int nb, const int32_t* __restrict__ cntq,
+                                                         const int32_t* __restrict__ cntk, int32_t* __restrict__ ordq,
+                                                         int32_t* __restrict__ ordk, int* __restrict__ counters) {
+    extern __shared__ int go_start[];   // [nb + 1]
+    const int dir = static_cast<int>(blockIdx.x) / BH, bh = static_cast<int>(blockIdx.x) - dir * BH;
+    const int32_t* cnt = (dir ? cntk : cntq) + static_cast<long long>(bh) * ngroups;
+    int32_t* ord = (dir ? ordk : ordq) + static_cast<long long>(bh) * ngroups;
+    if (bh == 0 && threadIdx.x == 0) counters[dir] = 0;
+    for (int i = threadIdx.x; i <= nb; i += blockDim.x) go_start[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < ngroups; i += blockDim.x) atomicAdd(&go_start[nb - cnt[i]], 1);
+    __syncthreads();
+    if (threadIdx.x < 32) {   // exclusive scan over descending lengths
+        int base = 0;
+        for (int i0 = 0; i0 <= nb; i0 += 32) {
+            const int i = i0 + threadIdx.x;
+            const int c = i <= nb ? go_start[i] : 0;
+            int incl = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (static_cast<int>(threadIdx.x) >= o) incl += y;
+            }
+            if (i <= nb) go_start[i] = base + incl - c;
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < ngroups; i += blockDim.x) ord[atomicAdd(&go_start[nb - cnt[i]], 1)] = i;
+}
+
+// Every block's real extent.
+__global__ void __launch_bounds__(256) grad_extent_kernel(Geo g, int32_t* __restrict__ ext) {
+    const int b = blockIdx.x * 256 + threadIdx.x;
+    if (b < g.nb) ext[b] = grad_extent(g, b);
+}
+
+// ------------------------------------------------------------------ host side
+
+struct GradWs {
+    size_t nlse2, ndelta, bits, ulq, ulk, cntq, cntk, ordq, ordk, ext, counters, total;
+    int G, ngroups, nwords;
+};
+
+static GradWs grad_ws(const fvattn_geom& g) {
+    auto al = [](size_t x) { return (x + 255) / 256 * 256; };
+    GradWs w;
+    const size_t BH = static_cast<size_t>(g.B) * g.H, nb = static_cast<size_t>(g.nb);
+    w.G = g.bs > 0 ? 128 / g.bs : 1;
+    w.ngroups = (g.nb + w.G - 1) / w.G;
+    w.nwords = (g.nb + 31) / 32;
+    const size_t units = BH * w.ngroups;
+    w.nlse2 = 0;
+    w.ndelta = w.nlse2 + al(4 * BH * g.Npad);
+    w.bits = w.ndelta + al(4 * BH * g.Npad);
+    w.ulq = w.bits + al(4 * BH * nb * w.nwords);
+    w.ulk = w.ulq + al(4 * units * nb);
+    w.cntq = w.ulk + al(4 * units * nb);
+    w.cntk = w.cntq + al(4 * units);
+    w.ordq = w.cntk + al(4 * units);
+    w.ordk = w.ordq + al(4 * units);
+    w.ext = w.ordk + al(4 * units);
+    w.counters = w.ext + al(4 * nb);
+    w.total = w.counters + 256;
+    return w;
+}
+
+template <int D, bool KV>
+static int launch_grad(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
+                       const GradArgs& args, int grid, cudaStream_t s) {
+    using L = GradSmem<D>;
+    if (cudaFuncSetAttribute(grad_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(L::ALLOC)) != cudaSuccess)
+        return FVATTN_ERR_CUDA;
+    // setmaxnreg waits for ever for registers that the CTA was not launched with
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, grad_kernel<D, KV>) != cudaSuccess) return FVATTN_ERR_CUDA;
+    if (static_cast<long long>(fa.numRegs) * GRAD_THREADS < 128ll * GRAD_LOW + 256ll * GRAD_HIGH)
+        return FVATTN_ERR_UNSUPPORTED;
+    grad_kernel<D, KV><<<grid, GRAD_THREADS, L::ALLOC, s>>>(a0, a1, b0, b1, args);
+    FV_CHECK_LAUNCH();
+    return FVATTN_OK;
+}
+
+template <int D>
+static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const void* k_t, const void* v_t,
+                         const void* o_t, const void* do_t, const float* lse, const int32_t* kv_idx,
+                         const int32_t* kv_cnt, float scale, void* dq_t, void* dk_t, void* dv_t, char* ws,
+                         cudaStream_t s) {
+    const int BH = g.B * g.H;
+    const long long rows = static_cast<long long>(BH) * g.Npad;
+    float* nlse2 = reinterpret_cast<float*>(ws + wl.nlse2);
+    float* ndelta = reinterpret_cast<float*>(ws + wl.ndelta);
+    uint32_t* bits = reinterpret_cast<uint32_t*>(ws + wl.bits);
+    uint32_t* ulq = reinterpret_cast<uint32_t*>(ws + wl.ulq);
+    uint32_t* ulk = reinterpret_cast<uint32_t*>(ws + wl.ulk);
+    int32_t* cntq = reinterpret_cast<int32_t*>(ws + wl.cntq);
+    int32_t* cntk = reinterpret_cast<int32_t*>(ws + wl.cntk);
+    int32_t* ordq = reinterpret_cast<int32_t*>(ws + wl.ordq);
+    int32_t* ordk = reinterpret_cast<int32_t*>(ws + wl.ordk);
+    int32_t* ext = reinterpret_cast<int32_t*>(ws + wl.ext);
+    int* counters = reinterpret_cast<int*>(ws + wl.counters);
+
+    CUtensorMap tq, tk, tv, tdo;
+    auto tmap = [&](CUtensorMap* m, const void* base) {
+        return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, static_cast<unsigned long long>(rows), D, 64u,
+                            static_cast<unsigned>(g.bs));
+    };
+    if (!tmap(&tq, q_t) || !tmap(&tk, k_t) || !tmap(&tv, v_t) || !tmap(&tdo, do_t)) return FVATTN_ERR_CUDA;
+    int dev = 0, nsm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return FVATTN_ERR_CUDA;
+
+    const int stat_blocks = static_cast<int>((rows + 63) / 64);
+    const int bit_blocks = static_cast<int>((static_cast<long long>(BH) * g.nb + 7) / 8);
+    grad_prep_kernel<D><<<stat_blocks + bit_blocks, 256, sizeof(uint32_t) * 8 * wl.nwords, s>>>(
+        g, stat_blocks, wl.nwords, static_cast<const uint4*>(o_t), static_cast<const uint4*>(do_t), lse, kv_idx, kv_cnt,
+        nlse2, ndelta, bits);
+    FV_CHECK_LAUNCH();
+    grad_extent_kernel<<<(g.nb + 255) / 256, 256, 0, s>>>(g, ext);
+    FV_CHECK_LAUNCH();
+    grad_lists_kernel<<<static_cast<unsigned>((2ll * BH * wl.ngroups + 7) / 8), 256, 0, s>>>(
+        g, wl.G, wl.ngroups, wl.nwords, bits, ulq, cntq, ulk, cntk);
+    FV_CHECK_LAUNCH();
+    grad_order_kernel<<<2 * BH, 256, sizeof(int) * (g.nb + 1), s>>>(BH, wl.ngroups, g.nb, cntq, cntk, ordq, ordk,
+                                                                    counters);
+    FV_CHECK_LAUNCH();
+
+    GradArgs a;
+    a.g = g;
+    a.G = wl.G;
+    a.ngroups = wl.ngroups;
+    a.ext = ext;
+    a.nlse2 = nlse2;
+    a.ndelta = ndelta;
+    a.scale = scale;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.total_items = BH * wl.ngroups;
+    a.oob_row = static_cast<int>(rows);
+    a.wait_limit_ns = WAIT_LIMIT_NS;
+    const int grid = nsm < a.total_items ? nsm : a.total_items;
+    a.ul = ulk;
+    a.cnt = cntk;
+    a.order = ordk;
+    a.counter = counters + 1;
+    a.out0 = static_cast<__nv_bfloat16*>(dv_t);
+    a.out1 = static_cast<__nv_bfloat16*>(dk_t);
+    int rc = launch_grad<D, true>(tk, tv, tq, tdo, a, grid, s);
+    if (rc != FVATTN_OK) return rc;
+    a.ul = ulq;
+    a.cnt = cntq;
+    a.order = ordq;
+    a.counter = counters;
+    a.out0 = static_cast<__nv_bfloat16*>(dq_t);
+    a.out1 = nullptr;
+    return launch_grad<D, false>(tq, tdo, tk, tv, a, grid, s);
+}
+
+}  // namespace fv
+
+using namespace fv;
+
+extern "C" size_t fvattn_sparse_attn_bwd_workspace_size(const fvattn_geom* gp) {
+    if (!gp) return 0;
+    return grad_ws(*gp).total;
+}
+
+extern "C" int fvattn_sparse_attn_bwd(const fvattn_geom* gp, const void* q_t, const void* k_t, const void* v_t,
+                                      const void* o_t, const void* do_t, const float* lse, const int32_t* kv_idx,
+                                      const int32_t* kv_cnt, float scale, void* dq_t, void* dk_t, void* dv_t,
+                                      void* workspace, size_t ws_bytes, fvattn_stream_t stream) {
+    const void* ptrs[] = {q_t, k_t, v_t, o_t, do_t, lse, kv_idx, kv_cnt, dq_t, dk_t, dv_t, workspace};
+    if (!gp) return FVATTN_ERR_INVALID;
+    for (const void* p : ptrs)
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 15u) != 0) return FVATTN_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FVATTN_ERR_INVALID;
+    if (!isfinite(scale) || !(scale > 0.f)) return FVATTN_ERR_INVALID;
+    if (gp->D != 64 && gp->D != 128) return FVATTN_ERR_UNSUPPORTED;
+    if (gp->bs != 16 && gp->bs != 32 && gp->bs != 64 && gp->bs != 128) return FVATTN_ERR_UNSUPPORTED;
+    if (gp->nb <= 0 || gp->nb > 2560) return FVATTN_ERR_UNSUPPORTED;
+    const long long rows = static_cast<long long>(gp->B) * gp->H * gp->Npad;
+    if (rows >= (1ll << 31)) return FVATTN_ERR_UNSUPPORTED;
+    const GradWs wl = grad_ws(*gp);
+    if (ws_bytes < wl.total) return FVATTN_ERR_INVALID;
+    const Geo g = to_geo(*gp);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    return gp->D == 128 ? grad_launches<128>(g, wl, q_t, k_t, v_t, o_t, do_t, lse, kv_idx, kv_cnt, scale, dq_t, dk_t,
+                                             dv_t, ws, s)
+                        : grad_launches<64>(g, wl, q_t, k_t, v_t, o_t, do_t, lse, kv_idx, kv_cnt, scale, dq_t, dk_t,
+                                            dv_t, ws, s);
+}
+
+int fv::take_status_grad() { return fv::take_tu_status(); }
