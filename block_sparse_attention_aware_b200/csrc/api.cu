@@ -106,7 +106,10 @@ extern "C" int fvattn_get_status(fvattn_stream_t stream) {
     const int va = take_status_attn();
     const int vr = take_status_route();
     const int vg = take_status_grad();
-    return va != FVATTN_OK ? va : (vr != FVATTN_OK ? vr : vg);
+    const int vc = take_status_cache();
+    for (const int v : {va, vr, vg})
+        if (v != FVATTN_OK) return v;
+    return vc;
 }
 
 extern "C" const char* fvattn_status_string(int code) {

@@ -1,0 +1,697 @@
+// A paged cache of keys and values: append with rotation, and the attention
+// of one new token a sequence over it.
+//
+// Append moves every new key, value and query once: a bit copy of V and
+// (a, b) -> (a c - b s, a s + b c) on the pairs of K and Q, bound by memory.
+//
+// Attention of one token reads each cached key and value once for a handful
+// of multiply-adds: bound by memory too, so the kernel's whole form follows
+// from keeping enough of the cache in flight.  One CTA takes one key head of
+// one sequence and a part of its tokens: a producer warp TMA-loads 64-token
+// tiles of K and V through the page table into a ring of shared memory, four
+// warps take 16 tokens of a tile each and keep an online softmax of their own
+// (running maximum, sum and O in registers), and the four are joined at the
+// end.  The heads that share a key head ride along in one product:
+//   S^T [16 tokens x 8 heads] = K Q^T,  O^T [D x 8 heads] += V^T P^T
+// with mma.sync.m16n8k16 (8 heads an N tile; a tcgen05 tile would have 128
+// rows of which one to sixteen hold a query).  Long sequences are split into
+// parts, whose (maximum, sum, O) a second small kernel joins in part order.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "fvattn_cache.h"
+#include "ptx.cuh"
+#include "sync.cuh"
+#include "tmap.cuh"
+
+namespace fv {
+
+// ------------------------------------------------------------------ append
+
+struct AppendArgs {
+    int Hq, Hkv, page, pages, B, width, axes;
+    int pair_end[3];              // first pair past each axis
+    int rot_rows, halves;
+    long long k_stride, v_stride, q_stride, q_out_stride;
+    const int32_t *cu, *lens, *table, *pos;
+    const float* rot;
+    const __nv_bfloat16 *k, *v, *q;
+    __nv_bfloat16 *q_out, *k_pages, *v_pages;
+};
+
+// A thread moves 16 elements (eight pairs, two 16-byte vectors) of one head.
+template <int D>
+__global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
+    constexpr int UPH = D / 16;          // such units a head
+    __shared__ __align__(16) float cs[D];
+    __shared__ int s_seq, s_ok;
+    __shared__ long long s_row;          // first element of the token's row in its page (head 0)
+    const long long t = blockIdx.x;
+    const int tid = threadIdx.x;
+    bool bad = false;                    // a position outside the rotation table
+    if (tid < 32) {
+        // the token's sequence: how many sequences end at or before it
+        int b = 0;
+        if (a.cu) {
+            for (int i = tid; i < a.B; i += 32) b += __ldg(a.cu + i + 1) <= t;
+            b = __reduce_add_sync(0xffffffffu, b);
+        } else {
+            b = t < a.B ? static_cast<int>(t) : a.B;
+        }
+        if (tid == 0) {
+            int ok = 0;
+            long long row = -1;
+            if (b < a.B) {
+                const int end = a.cu ? __ldg(a.cu + b + 1) : static_cast<int>(t) + 1;
+                const long long n = static_cast<long long>(__ldg(a.lens + b)) - (end - t);
+                int pg = -1;
+                if (n >= 0 && n < static_cast<long long>(a.width) * a.page)
+                    pg = __ldg(a.table + static_cast<long long>(b) * a.width + n / a.page);
+                if (pg >= 0 && pg < a.pages) {
+                    row = (static_cast<long long>(pg) * a.Hkv * a.page + n % a.page) * D;
+                    ok = 1;
+                } else {
+                    record_status(FVATTN_ERR_BOUNDS);
+                }
+            }
+            s_ok = ok;
+            s_row = row;
+        }
+    } else if (a.rot && tid - 32 < D) {
+        // this token's cosines and sines, by the pair's axis
+        const int e = tid - 32, i = e < D / 2 ? e : e - D / 2;
+        int ax = 0;
+        while (ax < a.axes - 1 && i >= a.pair_end[ax]) ++ax;
+        // rows behind the last sequence have no position to read
+        const bool live = t < (a.cu ? __ldg(a.cu + a.B) : a.B);
+        const int n = live ? __ldg(a.pos + t * a.axes + ax) : 0;
+        if (n >= 0 && n < a.rot_rows) {
+            cs[e] = __ldg(a.rot + static_cast<long long>(n) * D + e);
+        } else {
+            record_status(FVATTN_ERR_BOUNDS);
+            bad = true;
+        }
+    }
+    if (__syncthreads_or(bad) || !s_ok) return;
+    const int u = tid % UPH;
+    const int step = a.halves ? D / 2 : 8;       // distance of the unit's two vectors
+    const int e0 = a.halves ? 8 * u : 16 * u;
+    float c[8], s[8];
+    if (a.rot) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            c[i] = cs[8 * u + i];
+            s[i] = cs[D / 2 + 8 * u + i];
+        }
+    }
+    const int heads = a.Hq + 2 * a.Hkv;
+    const int per = 256 / UPH;
+    for (int vh = blockIdx.y * per + tid / UPH; vh < heads; vh += gridDim.y * per) {
+        const bool is_q = vh < a.Hq, is_v = vh >= a.Hq + a.Hkv;
+        const int h = is_q ? vh : (is_v ? vh - a.Hq - a.Hkv : vh - a.Hq);
+        const __nv_bfloat16* src = is_q ? a.q + t * a.q_stride : (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride);
+        src += static_cast<long long>(h) * D + e0;
+        __nv_bfloat16* dst = is_q ? a.q_out + t * a.q_out_stride + static_cast<long long>(h) * D
+                                  : (is_v ? a.v_pages : a.k_pages) + s_row + static_cast<long long>(h) * a.page * D;
+        dst += e0;
+        uint4 x = *reinterpret_cast<const uint4*>(src);
+        uint4 y = *reinterpret_cast<const uint4*>(src + step);
+        if (a.rot && !is_v) {
+            uint32_t xe[4] = {x.x, x.y, x.z, x.w}, ye[4] = {y.x, y.y, y.z, y.w};
+            if (a.halves) {      // x holds the pairs' first elements, y the second
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a0 = __uint_as_float(xe[i] << 16), a1 = __uint_as_float(xe[i] & 0xFFFF0000u);
+                    const float b0 = __uint_as_float(ye[i] << 16), b1 = __uint_as_float(ye[i] & 0xFFFF0000u);
+                    xe[i] = pack_bf16x2(a0 * c[2 * i] - b0 * s[2 * i], a1 * c[2 * i + 1] - b1 * s[2 * i + 1]);
+                    ye[i] = pack_bf16x2(a0 * s[2 * i] + b0 * c[2 * i], a1 * s[2 * i + 1] + b1 * c[2 * i + 1]);
+                }
+            } else {             // each 32-bit word is one pair
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a0 = __uint_as_float(xe[i] << 16), b0 = __uint_as_float(xe[i] & 0xFFFF0000u);
+                    const float a1 = __uint_as_float(ye[i] << 16), b1 = __uint_as_float(ye[i] & 0xFFFF0000u);
+                    xe[i] = pack_bf16x2(a0 * c[i] - b0 * s[i], a0 * s[i] + b0 * c[i]);
+                    ye[i] = pack_bf16x2(a1 * c[4 + i] - b1 * s[4 + i], a1 * s[4 + i] + b1 * c[4 + i]);
+                }
+            }
+            x = make_uint4(xe[0], xe[1], xe[2], xe[3]);
+            y = make_uint4(ye[0], ye[1], ye[2], ye[3]);
+        }
+        *reinterpret_cast<uint4*>(dst) = x;
+        *reinterpret_cast<uint4*>(dst + step) = y;
+    }
+}
+
+// ------------------------------------------------------------------ attention of one token
+
+constexpr int DEC_TILE = 64;            // tokens a ring stage
+constexpr int DEC_WARPS = 4;            // arithmetic warps, 16 tokens of a tile each
+constexpr int DEC_THREADS = 32 * (DEC_WARPS + 1);
+constexpr int DEC_CTAS = 2;             // CTAs an SM
+constexpr int DEC_MAX_PARTS = 128;
+
+template <int D>
+struct DecSmem {
+    static constexpr uint32_t TILE = DEC_TILE * D * 2u;          // D/64 halves of 8 KB, 128-byte swizzled rows
+    static constexpr int STAGES = D == 128 ? 3 : 6;              // 96 KB a CTA
+    static constexpr uint32_t K = 0, V = STAGES * TILE, BARS = 2 * STAGES * TILE;
+    static constexpr uint32_t TOTAL = BARS + 16u * STAGES + 16u;
+};
+
+struct DecArgs {
+    int Hq, Hkv, group, gchunks, page, pages, width, tokens, parts;
+    long long longest, q_stride;
+    const __nv_bfloat16* q;
+    const int32_t *table, *lens;
+    float scale_log2;
+    __nv_bfloat16* o;
+    float* lse;
+    float2* part_ml;       // [B][Hq][parts] (maximum in log2 units, sum)
+    float* part_o;         // [B][Hq][parts][D], relative to the maximum
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A sequence's length, range-checked.
+__device__ __forceinline__ int cache_len(const DecArgs& a, int b) {
+    const int n = __ldg(a.lens + b);
+    const long long cap = min(a.longest, static_cast<long long>(a.width) * a.page);
+    if (n < 0 || n > cap) {
+        record_status(FVATTN_ERR_BOUNDS);
+        return n < 0 ? 0 : static_cast<int>(cap);
+    }
+    return n;
+}
+
+// NT: tiles of 8 query heads (heads that share this key head, up to 16 a CTA).
+template <int D, int NT>
+__global__ void __launch_bounds__(DEC_THREADS, DEC_CTAS)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const DecArgs a) {
+    using L = DecSmem<D>;
+    constexpr int NS = L::STAGES;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ int s_abort;
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = blockIdx.x;
+    const int hk = blockIdx.y / a.gchunks, gc = blockIdx.y - hk * a.gchunks;
+    const int b = blockIdx.z;
+    const int head0 = hk * a.group + gc * 16;                 // first query head of this CTA
+    const int nheads = min(16, a.group - gc * 16);
+    pdl_launch_dependents();
+    const int len = cache_len(a, b);
+    const int t0 = part * a.tokens;
+    const int t1 = min(len, t0 + a.tokens);
+    if (t1 <= t0) {
+        // an empty part is not read by the join; an unsplit empty sequence is answered here
+        if (a.parts == 1)
+            for (int i = threadIdx.x; i < nheads * D; i += DEC_THREADS) {
+                const long long at = static_cast<long long>(b) * a.Hq + head0 + i / D;
+                a.o[at * D + i % D] = __float2bfloat16(0.f);
+                if (a.lse && i % D == 0) a.lse[at] = -INFINITY;
+            }
+        return;
+    }
+    if (sbase & 1023u) {   // the 128-byte swizzle needs 1024-byte aligned tiles
+        if (threadIdx.x == 0) record_status(FVATTN_ERR_UNSUPPORTED);
+        return;
+    }
+    unsigned long long* full = reinterpret_cast<unsigned long long*>(smem + L::BARS);
+    unsigned long long* empty = full + NS;
+    volatile int* abort_flag = &s_abort;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(smem_u32(full + s), 1);
+            mbar_init(smem_u32(empty + s), DEC_WARPS);
+        }
+        s_abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const int tiles = (t1 - t0 + DEC_TILE - 1) / DEC_TILE;
+
+    float o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][d][i] = 0.f;
+    }
+
+    if (warp == DEC_WARPS) {
+        // =========================== producer
+        const int box = min(a.page, DEC_TILE);           // rows a load
+        const int boxes = DEC_TILE / box;
+        const int32_t* row = a.table + static_cast<long long>(b) * a.width;
+        int it = 0;
+        for (; it < tiles; ++it) {
+            const int st = it % NS;
+            const int tok = t0 + it * DEC_TILE + lane * box;
+            int pg = 0;
+            const bool mine = lane < boxes && tok < t1;
+            if (mine) {
+                pg = __ldg(row + tok / a.page);
+                if (pg < 0 || pg >= a.pages) {
+                    record_status(FVATTN_ERR_BOUNDS);
+                    pg = 0;
+                }
+            }
+            if (!wait_warp(smem_u32(empty + st), ((it / NS) & 1) ^ 1, abort_flag)) break;
+            const int nbox = __popc(__ballot_sync(0xffffffffu, mine));
+            if (lane == 0) mbar_arrive_expect_tx(smem_u32(full + st), static_cast<uint32_t>(2 * nbox * box * D * 2));
+            __syncwarp();
+            if (mine) {
+                const int r = (pg * a.Hkv + hk) * a.page + tok % a.page;
+                const uint32_t off = st * L::TILE + static_cast<uint32_t>(lane * box) * 128u;
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                    tma_load_2d(sbase + L::K + off + h * 8192u, &tmK, h * 64, r, smem_u32(full + st));
+                    tma_load_2d(sbase + L::V + off + h * 8192u, &tmV, h * 64, r, smem_u32(full + st));
+                }
+            }
+        }
+        // no copy outlives the CTA
+        if (lane == 0)
+            for (int st = 0; st < NS && st < it; ++st)
+                wait_bar_drain(smem_u32(full + st), (((it - 1 - st) / NS) & 1));
+        __syncwarp();
+    } else {
+        // =========================== arithmetic: 16 tokens of each tile
+        const int g = lane >> 2, tq = lane & 3;
+        uint32_t qf[NT][D / 16][2];        // Q^T: head g of the tile, elements 2 tq .. of each 16
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int h = n * 8 + g;
+            const __nv_bfloat16* qr = a.q + static_cast<long long>(b) * a.q_stride + static_cast<long long>(head0 + h) * D;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    qf[n][kk][i] = h < nheads ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + i * 8 + 2 * tq)) : 0u;
+        }
+        for (int it = 0; it < tiles; ++it) {
+            const int st = it % NS;
+            if (!wait_warp(smem_u32(full + st), (it / NS) & 1, abort_flag)) break;
+            const int left = t1 - (t0 + it * DEC_TILE + warp * 16);    // tokens of this warp's 16 that exist
+            if (left > 0) {
+                const uint32_t kt = sbase + L::K + st * L::TILE, vt = sbase + L::V + st * L::TILE;
+                float s[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+                {
+                    const int r = warp * 16 + (lane & 15);
+                    const uint32_t rb = kt + static_cast<uint32_t>(r) * 128u;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        uint32_t af[4];
+                        ldsm_x4(af, rb + (kk >> 2) * 8192u + ((((kk & 3) * 2 + (lane >> 4)) ^ (r & 7)) * 16u));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_16816(s[n], af, qf[n][kk][0], qf[n][kk][1]);
+                    }
+                }
+                // token g: s[.][0..1], token g + 8: s[.][2..3]; heads 2 tq, 2 tq + 1 of the tile
+                const bool v0 = g < left, v1 = g + 8 < left;
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float x0 = v0 ? s[n][i] * a.scale_log2 : -INFINITY;
+                        const float x1 = v1 ? s[n][2 + i] * a.scale_log2 : -INFINITY;
+                        float mx = fmaxf(x0, x1);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        const float mn = fmaxf(m[n][i], mx);
+                        const float ref = mn == -INFINITY ? 0.f : mn;      // scores of -inf only: P is 0
+                        const float alpha = ex2_approx(m[n][i] - ref);
+                        const float p0 = ex2_approx(x0 - ref), p1 = ex2_approx(x1 - ref);
+                        l[n][i] = l[n][i] * alpha + p0 + p1;
+                        m[n][i] = mn;
+                        s[n][i] = p0;
+                        s[n][2 + i] = p1;
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d) {
+                            o[n][d][i] *= alpha;
+                            o[n][d][2 + i] *= alpha;
+                        }
+                    }
+                    pb[n][0] = movm_t(pack_bf16x2(s[n][0], s[n][1]));
+                    pb[n][1] = movm_t(pack_bf16x2(s[n][2], s[n][3]));
+                }
+                // values of tokens that do not exist are taken as 0 (0 times what is there could be NaN);
+                // lane words hold tokens 2 tq, 2 tq + 1 (words 0, 1) and 8 further (words 2, 3)
+                const uint32_t k0 = (2 * tq < left ? 0x0000FFFFu : 0u) | (2 * tq + 1 < left ? 0xFFFF0000u : 0u);
+                const uint32_t k1 = (2 * tq + 8 < left ? 0x0000FFFFu : 0u) | (2 * tq + 9 < left ? 0xFFFF0000u : 0u);
+                const int r = warp * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
+                const uint32_t rb = vt + static_cast<uint32_t>(r) * 128u;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    uint32_t af[4];
+                    ldsm_x4_t(af, rb + (d >> 2) * 8192u + ((((d & 3) * 2 + ((lane >> 3) & 1)) ^ (r & 7)) * 16u));
+                    if (left < 16) {
+                        af[0] &= k0;
+                        af[1] &= k0;
+                        af[2] &= k1;
+                        af[3] &= k1;
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_16816(o[n][d], af, pb[n][0], pb[n][1]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(empty + st));
+        }
+    }
+
+    // ---- join the four warps through the ring's memory (every load has landed)
+    __syncthreads();
+    if (*abort_flag) return;
+    float* jm = reinterpret_cast<float*>(smem);                  // [warp][16] maximum
+    float* jl = jm + DEC_WARPS * 16;                             // [warp][16] sum
+    float* jo = jl + DEC_WARPS * 16;                             // [warp][head][D + 4]
+    constexpr int JP = D + 4;
+    static_assert((2 * DEC_WARPS * 16 + DEC_WARPS * 16 * JP) * 4 <= L::BARS, "join buffer");
+    if (warp < DEC_WARPS) {
+        const int g = lane >> 2, tq = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float sum = l[n][i];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                const int h = n * 8 + 2 * tq + i;
+                if (g == 0) {
+                    jm[warp * 16 + h] = m[n][i];
+                    jl[warp * 16 + h] = sum;
+                }
+                float* dst = jo + (warp * 16 + h) * JP;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    dst[d * 16 + g] = o[n][d][i];
+                    dst[d * 16 + 8 + g] = o[n][d][2 + i];
+                }
+            }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nheads * D; i += DEC_THREADS) {
+        const int h = i / D, d = i - h * D;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < DEC_WARPS; ++w) mx = fmaxf(mx, jm[w * 16 + h]);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < DEC_WARPS; ++w) {
+            const float f = ex2_approx(jm[w * 16 + h] - ref);
+            sum += jl[w * 16 + h] * f;
+            acc += jo[(w * 16 + h) * JP + d] * f;
+        }
+        const long long at = static_cast<long long>(b) * a.Hq + head0 + h;
+        if (a.parts == 1) {
+            a.o[at * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
+            if (a.lse && d == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+        } else {
+            const long long pt = at * a.parts + part;
+            a.part_o[pt * D + d] = acc;
+            if (d == 0) a.part_ml[pt] = make_float2(mx, sum);
+        }
+    }
+}
+
+// One warp per (sequence, query head): join the parts that hold tokens.
+template <int D>
+__global__ void __launch_bounds__(128) cache_join_kernel(const DecArgs a, int heads) {
+    const int lane = threadIdx.x & 31;
+    const int at = blockIdx.x * 4 + (threadIdx.x >> 5);
+    pdl_wait();
+    if (at >= heads) return;
+    const int len = cache_len(a, at / a.Hq);
+    const int n = (len + a.tokens - 1) / a.tokens;
+    const float2* ml = a.part_ml + static_cast<long long>(at) * a.parts;
+    const float* po = a.part_o + static_cast<long long>(at) * a.parts * D;
+    float mx = -INFINITY;
+    for (int p = lane; p < n; p += 32) mx = fmaxf(mx, ml[p].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    constexpr int V = D / 32;          // elements a lane
+    float acc[V], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < n; ++p) {
+        const float2 x = ml[p];
+        const float f = ex2_approx(x.x - ref);
+        sum += x.y * f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += po[static_cast<long long>(p) * D + i * 32 + lane] * f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        a.o[static_cast<long long>(at) * D + i * 32 + lane] = __float2bfloat16(sum == 0.f ? 0.f : acc[i] / sum);
+    if (a.lse && lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------ host side
+
+static bool cache_ok(const fvattn_cache* c) {
+    return c && c->k && c->v && ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15u) == 0 &&
+           c->k != c->v && c->pages > 0 && c->Hkv > 0;
+}
+
+static bool cache_supported(int D, int page) {
+    return (D == 64 || D == 128) && (page == 16 || page == 32 || page == 64 || page == 128);
+}
+
+static bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+static bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The split: as many parts as fill the GPU's CTA slots without a nearly empty
+// last round, at least 256 tokens a part.
+static int split_parts(int B, int Hq, int Hkv, long long longest, int nsm, int* tokens) {
+    const int gchunks = (Hq / Hkv + 15) / 16;
+    const long long base = static_cast<long long>(B) * Hkv * gchunks;
+    const long long slots = static_cast<long long>(nsm) * DEC_CTAS;
+    long long most = (longest + 255) / 256;
+    if (most < 1) most = 1;
+    if (most > DEC_MAX_PARTS) most = DEC_MAX_PARTS;
+    double best = 1e300;
+    auto time = [&](long long n) {
+        const double rounds = static_cast<double>((base * n + slots - 1) / slots);
+        const double chunk = static_cast<double>((longest + n - 1) / n);
+        return rounds * (chunk + 200.0);       // a CTA's fixed cost is that of about 200 tokens
+    };
+    for (long long n = 1; n <= most; ++n)
+        if (time(n) < best) best = time(n);
+    long long pick = 1;
+    for (long long n = 1; n <= most; ++n)
+        if (time(n) <= 1.05 * best) pick = n;
+    long long tk = (longest + pick - 1) / pick;
+    tk = (tk + DEC_TILE - 1) / DEC_TILE * DEC_TILE;
+    if (tk < DEC_TILE) tk = DEC_TILE;
+    *tokens = static_cast<int>(tk);
+    const long long parts = (longest + tk - 1) / tk;
+    return parts < 1 ? 1 : static_cast<int>(parts);
+}
+
+static int current_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+    return n;
+}
+
+template <int D, int NT>
+static int launch_cache_attn(const CUtensorMap& tk, const CUtensorMap& tv, const DecArgs& a, int B, cudaStream_t s) {
+    using L = DecSmem<D>;
+    if (cudaFuncSetAttribute(cache_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(L::TOTAL)) != cudaSuccess)
+        return FVATTN_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>(a.parts), static_cast<unsigned>(a.Hkv * a.gchunks), static_cast<unsigned>(B));
+    cache_attn_kernel<D, NT><<<grid, DEC_THREADS, L::TOTAL, s>>>(tk, tv, a);
+    FV_CHECK_LAUNCH();
+    if (a.parts == 1) return FVATTN_OK;
+    cudaLaunchConfig_t cfg = {};
+    const int heads = B * a.Hq;
+    cfg.gridDim = dim3(static_cast<unsigned>((heads + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, a, heads) != cudaSuccess) return FVATTN_ERR_CUDA;
+    return FVATTN_OK;
+}
+
+}  // namespace fv
+
+using namespace fv;
+
+extern "C" int fvattn_cache_append(const fvattn_cache* c, int B, long long rows, const int32_t* cu,
+                                   const int32_t* lens, const int32_t* table, int width, const void* k,
+                                   long long k_stride, const void* v, long long v_stride, const void* q,
+                                   long long q_stride, int Hq, void* q_out, long long q_out_stride,
+                                   const fvattn_rotation* rot, fvattn_stream_t stream) {
+    if (!cache_ok(c) || B < 1 || rows < 0 || rows > 0x7fffffffll || width < 1 || !lens || !table || !k || !v)
+        return FVATTN_ERR_INVALID;
+    if (!cache_supported(c->D, c->page)) return FVATTN_ERR_UNSUPPORTED;
+    if (!cu && rows < B) return FVATTN_ERR_INVALID;
+    if (!on16(k) || !on16(v) || !on4(lens) || !on4(table) || (cu && !on4(cu))) return FVATTN_ERR_INVALID;
+    const long long kv_row = static_cast<long long>(c->Hkv) * c->D;
+    if (k_stride < kv_row || v_stride < kv_row || k_stride % 8 || v_stride % 8) return FVATTN_ERR_INVALID;
+    if ((q == nullptr) != (q_out == nullptr)) return FVATTN_ERR_INVALID;
+    if (q) {
+        const long long q_row = static_cast<long long>(Hq) * c->D;
+        if (Hq < 1 || !on16(q) || !on16(q_out) || q_stride < q_row || q_out_stride < q_row || q_stride % 8 ||
+            q_out_stride % 8)
+            return FVATTN_ERR_INVALID;
+    }
+    AppendArgs a = {};
+    if (rot) {
+        if (!rot->table || !on16(rot->table) || !rot->pos || !on4(rot->pos) || rot->rows < 1 || rot->axes < 1 ||
+            rot->axes > 3 || (rot->halves != 0 && rot->halves != 1))
+            return FVATTN_ERR_INVALID;
+        int end = 0;
+        for (int i = 0; i < rot->axes; ++i) {
+            if (rot->pairs[i] < 0 || rot->pairs[i] > c->D / 2) return FVATTN_ERR_INVALID;
+            end += rot->pairs[i];
+            a.pair_end[i] = end;
+        }
+        if (end != c->D / 2) return FVATTN_ERR_INVALID;
+        a.axes = rot->axes;
+        a.rot_rows = rot->rows;
+        a.halves = rot->halves;
+        a.rot = rot->table;
+        a.pos = rot->pos;
+    }
+    if (rows == 0) return FVATTN_OK;
+    a.Hq = q ? Hq : 0;
+    a.Hkv = c->Hkv;
+    a.page = c->page;
+    a.pages = c->pages;
+    a.B = B;
+    a.width = width;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_stride = q_stride;
+    a.q_out_stride = q_out_stride;
+    a.cu = cu;
+    a.lens = lens;
+    a.table = table;
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.q_out = static_cast<__nv_bfloat16*>(q_out);
+    a.k_pages = static_cast<__nv_bfloat16*>(c->k);
+    a.v_pages = static_cast<__nv_bfloat16*>(c->v);
+    // few tokens: their heads over several CTAs
+    const int per = 256 / (c->D / 16);
+    const int passes = (a.Hq + 2 * a.Hkv + per - 1) / per;
+    const dim3 grid(static_cast<unsigned>(rows), rows < 512 ? static_cast<unsigned>(passes < 64 ? passes : 64) : 1u);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (c->D == 128)
+        cache_append_kernel<128><<<grid, 256, 0, s>>>(a);
+    else
+        cache_append_kernel<64><<<grid, 256, 0, s>>>(a);
+    FV_CHECK_LAUNCH();
+    return FVATTN_OK;
+}
+
+extern "C" int fvattn_cache_attn_parts(int B, int Hq, int Hkv, int D, long long longest, int* tokens) {
+    if (B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || (D != 64 && D != 128) || longest < 0 || longest > 0x7fffffffll - 128)
+        return 0;
+    int tk = 0;
+    const int parts = split_parts(B, Hq, Hkv, longest, current_sms(), &tk);
+    if (tokens) *tokens = tk;
+    return parts;
+}
+
+extern "C" size_t fvattn_cache_attn_workspace_size(int B, int Hq, int Hkv, int D, long long longest) {
+    const int parts = fvattn_cache_attn_parts(B, Hq, Hkv, D, longest, nullptr);
+    if (parts < 2) return 0;
+    const size_t n = static_cast<size_t>(B) * Hq * parts;
+    return (n * 8 + 255) / 256 * 256 + n * D * 4;
+}
+
+extern "C" int fvattn_cache_attn(const fvattn_cache* c, int B, int Hq, const void* q, long long q_stride,
+                                 const int32_t* table, int width, const int32_t* lens, long long longest, float scale,
+                                 void* o, float* lse, void* workspace, size_t ws_bytes, fvattn_stream_t stream) {
+    if (!cache_ok(c) || B < 1 || B > 65535 || width < 1 || !q || !table || !lens || !o) return FVATTN_ERR_INVALID;
+    if (!cache_supported(c->D, c->page)) return FVATTN_ERR_UNSUPPORTED;
+    if (Hq < c->Hkv || Hq % c->Hkv || longest < 0 || longest > 0x7fffffffll - 128) return FVATTN_ERR_INVALID;
+    if (!on16(q) || !on16(o) || !on4(table) || !on4(lens) || (lse && !on4(lse))) return FVATTN_ERR_INVALID;
+    if (q_stride < static_cast<long long>(Hq) * c->D || q_stride % 8) return FVATTN_ERR_INVALID;
+    if (!isfinite(scale) || !(scale > 0.f)) return FVATTN_ERR_INVALID;
+    const long long rows = static_cast<long long>(c->pages) * c->Hkv * c->page;
+    if (rows >= (1ll << 31)) return FVATTN_ERR_UNSUPPORTED;
+    DecArgs a = {};
+    a.Hq = Hq;
+    a.Hkv = c->Hkv;
+    a.group = Hq / c->Hkv;
+    a.gchunks = (a.group + 15) / 16;
+    if (static_cast<long long>(a.Hkv) * a.gchunks > 65535 || static_cast<long long>(B) * Hq > 0x7fffffffll)
+        return FVATTN_ERR_UNSUPPORTED;
+    a.parts = split_parts(B, Hq, c->Hkv, longest, current_sms(), &a.tokens);
+    if (a.parts > 1) {
+        const size_t need = fvattn_cache_attn_workspace_size(B, Hq, c->Hkv, c->D, longest);
+        if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < need)
+            return FVATTN_ERR_INVALID;
+        const size_t n = static_cast<size_t>(B) * Hq * a.parts;
+        a.part_ml = static_cast<float2*>(workspace);
+        a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + (n * 8 + 255) / 256 * 256);
+    }
+    a.page = c->page;
+    a.pages = c->pages;
+    a.width = width;
+    a.longest = longest;
+    a.q_stride = q_stride;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.table = table;
+    a.lens = lens;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.o = static_cast<__nv_bfloat16*>(o);
+    a.lse = lse;
+    CUtensorMap tk, tv;
+    const unsigned box = static_cast<unsigned>(c->page < DEC_TILE ? c->page : DEC_TILE);
+    if (!make_tmap_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c->k, static_cast<unsigned long long>(rows),
+                      static_cast<unsigned long long>(c->D), 64u, box) ||
+        !make_tmap_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c->v, static_cast<unsigned long long>(rows),
+                      static_cast<unsigned long long>(c->D), 64u, box))
+        return FVATTN_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool two = a.group > 8;
+    if (c->D == 128)
+        return two ? launch_cache_attn<128, 2>(tk, tv, a, B, s) : launch_cache_attn<128, 1>(tk, tv, a, B, s);
+    return two ? launch_cache_attn<64, 2>(tk, tv, a, B, s) : launch_cache_attn<64, 1>(tk, tv, a, B, s);
+}
+
+int fv::take_status_cache() { return fv::take_tu_status(); }

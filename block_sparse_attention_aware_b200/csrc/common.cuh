@@ -53,6 +53,7 @@ static inline int take_tu_status() {
 int take_status_route();
 int take_status_attn();
 int take_status_grad();
+int take_status_cache();
 
 // Raster tile index of a block, and block of a raster tile (identities in
 // raster tile order).
