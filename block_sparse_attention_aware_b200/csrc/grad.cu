@@ -6,21 +6,29 @@
 //   dP = dO V^T,  dS = P (dP - delta),  delta_t = dO_t . O_t
 //   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
 //
-// Two passes over the pairs, one that keeps a key tile in place and sums dK
-// and dV over the query blocks that keep it, one that keeps a query tile in
-// place and sums dQ over its kept key blocks.  S and dP are formed in both:
-// seven products where five would do if dQ were added up in memory by
-// atomics, whose order would change the result's bits, or if dS were stored
-// (32 KB a pair of blocks).  Every sum here runs in one CTA in list order.
+// Two passes over the pairs, one that keeps a query tile in place and sums dQ
+// over its kept key blocks, then one that keeps a key tile in place and sums
+// dK and dV over the query blocks that keep it.  S and dP are formed in both:
+// the other way, one pass, adds dQ up in memory by atomics, whose order would
+// change the result's bits, or stores dS (32 KB a pair of blocks).  Every sum
+// here runs in one CTA in list order.
+//
+// delta.  dP - delta cancels where a softmax is concentrated, and dO . O from
+// the bf16 O is then too coarse: with scores of standard deviation 3 the
+// gradients' error against 64 bits was 1.7 times that of rounding the result.
+// The query pass therefore starts from delta0 = dO . O and sums the exact
+// delta_t = sum_u P_tu dP_tu on the way; its dQ is put right at the end,
+//   dQ = scale (sum_u dS0_tu k_u - (delta - delta0) sum_u P_tu k_u),
+// for a product more, and the key pass reads the exact delta.
 //
 // Both passes are one kernel, grad_kernel<D, KV>, one CTA of 384 threads per
 // SM (it holds all 512 tensor-memory columns):
 //   warp 0      producer: takes items, TMA-loads the item's own tile pair
 //               (KV: K and V; else Q and dO), streams the first tensor of the
 //               other side (KV: Q; else K) in chunks of 128 rows and writes
-//               each chunk's mask words
+//               each chunk's masks
 //   warp 2      producer of the other streamed tensor (KV: dO; else V)
-//   warp 1      one lane issues every MMA
+//   warps 1, 3  one lane each issues MMAs
 //   warps 4..11 two groups of four warps; a thread has one row of the
 //               128-row tile and half of the chunk's 128 columns: P and dS
 //               are formed from the fp32 S and dP in tensor memory and go
@@ -28,11 +36,16 @@
 //               accumulating products
 // KV: rows are keys, columns queries (S^T, dP^T); columns' statistics come
 // with the stream.  Else rows are queries with their statistics in registers.
+// Per chunk i, in tensor memory (all 512 columns):
+//   S(i) -> P(i) over it, A0 += P(i) B;   dP(i) -> dS(i) over it, A1 += dS(i) B0
+// with KV: A0 = dV (B = dO), A1 = dK; else A0 = sum P k (B = B0), A1 = dQ.
 //
 // bs < 128: as in the forward, a tile holds G = 128 / bs consecutive blocks
 // and walks the union of their lists; a chunk packs 128 / bs listed blocks and
 // each row sees only the columns of blocks that its own block is paired with.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "fvattn_train.h"
@@ -43,7 +56,9 @@
 namespace fv {
 
 constexpr int GRAD_THREADS = 384;
-constexpr int GRAD_STAGES = 2;
+// The first streamed tensor is held from S to the last product of its chunk,
+// over one and a half chunks' time: a stage more.
+constexpr int GRAD_STAGES0 = 3, GRAD_STAGES1 = 2;
 constexpr uint32_t GRAD_TMEM = 512;
 constexpr int GRAD_GROUP = 8;     // blocks per tile at bs = 16
 // Register split (setmaxnreg): the launch gives 168 a thread; one warpgroup
@@ -51,10 +66,8 @@ constexpr int GRAD_GROUP = 8;     // blocks per tile at bs = 16
 constexpr int GRAD_LAUNCH_REGS = 168, GRAD_LOW = 72, GRAD_HIGH = 216;
 static_assert(128 * GRAD_LOW + 256 * GRAD_HIGH <= GRAD_THREADS * GRAD_LAUNCH_REGS, "register split");
 
-// Tensor-memory columns.  KV: S^T (P^T over it), dP^T (dS^T over it), dV, dK.
-// Else: two S buffers (dS over them), dP, dQ.
-constexpr uint32_t T_S = 0, T_DP_KV = 128, T_DV = 256, T_DK = 384;
-constexpr uint32_t T_DP_Q = 256, T_DQ = 384;
+// Tensor-memory columns: S (P over it), dP (dS over it), the two accumulators.
+constexpr uint32_t T_S = 0, T_DP = 128, T_A0 = 256, T_A1 = 384;
 
 struct GradArgs {
     Geo g;
@@ -65,7 +78,7 @@ struct GradArgs {
     int* counter;
     const int32_t* ext;       // [nb] real extent of each block
     const float* nlse2;       // [B*H][Npad] -lse * log2(e); -inf for rows that take no part
-    const float* ndelta;      // [B*H][Npad] -dO . O
+    float* ndelta;            // [B*H][Npad] -delta: read by KV; else -delta0, replaced by the exact one
     __nv_bfloat16* out0;      // KV: dV; else dQ
     __nv_bfloat16* out1;      // KV: dK
     float scale, scale_log2;
@@ -75,15 +88,19 @@ struct GradArgs {
 };
 
 struct __align__(16) GradCtrl {
-    float nlse2[GRAD_STAGES][128], ndelta[GRAD_STAGES][128];   // KV: the chunk's column statistics
-    uint32_t mask[GRAD_STAGES][GRAD_GROUP][4];                 // per block of the tile: columns its rows see
-    unsigned long long a_full, a_empty;                        // the item's own tile pair
-    unsigned long long b0_full[GRAD_STAGES], b0_empty[GRAD_STAGES];
-    unsigned long long b1_full[GRAD_STAGES], b1_empty[GRAD_STAGES];
-    unsigned long long s_full[2], dp_full, dp_free, p_full, ds_full[2];
+    // KV: the chunks' column statistics, -lse2 of the first ring's stages and then -delta of the second's.
+    // Else: sums of P dP by row, [item's parity][team]
+    float stat[GRAD_STAGES0 + GRAD_STAGES1][128];
+    uint32_t mask[GRAD_STAGES0][8];                              // 4 words of columns that are tokens, then a
+                                                                 // byte a slot: blocks of the tile paired with it
+    unsigned long long a_full, a_empty;                          // the item's own tile pair
+    unsigned long long b0_full[GRAD_STAGES0], b0_empty[GRAD_STAGES0];
+    unsigned long long b1_full[GRAD_STAGES1], b1_empty[GRAD_STAGES1];
+    unsigned long long s_full, dp_full, p_full[2], ds_full[2];
+    unsigned long long sum_full;
     unsigned long long acc_full, acc_free;
     unsigned long long item_full[2], item_empty[2];
-    unsigned long long drain;
+    unsigned long long drain[2];
     int item[2][4];            // bh, tile, list length, valid
     uint32_t tmem_base;
     int abort_flag;
@@ -92,8 +109,8 @@ struct __align__(16) GradCtrl {
 template <int D>
 struct GradSmem {
     static constexpr uint32_t TILE = 128u * D * 2u;
-    static constexpr uint32_t A0 = 0, A1 = TILE, B0 = 2 * TILE, B1 = B0 + GRAD_STAGES * TILE;
-    static constexpr uint32_t CTRL = B1 + GRAD_STAGES * TILE;
+    static constexpr uint32_t A0 = 0, A1 = TILE, B0 = 2 * TILE, B1 = B0 + GRAD_STAGES0 * TILE;
+    static constexpr uint32_t CTRL = B1 + GRAD_STAGES1 * TILE;
     static constexpr uint32_t TOTAL = CTRL + static_cast<uint32_t>(sizeof(GradCtrl));
     // at least 120 KB, so that two CTAs never share an SM's tensor memory
     static constexpr uint32_t ALLOC = TOTAL > 120u * 1024u ? TOTAL : 120u * 1024u;
@@ -119,12 +136,29 @@ __device__ __forceinline__ int grad_slot(const uint32_t* ul, int e, int cnt, uin
     return static_cast<int>(v & 0xFFFFFFu);
 }
 
+// Columns 64 w .. of a chunk that a row of the tile's block tb sees, 32 a
+// word: those of slots whose block is paired with tb, and tokens (unless
+// `all`).  lbs = log2(bs).
+__device__ __forceinline__ void grad_mask(const uint32_t* m, int lbs, int tb, int w, bool all, uint32_t (&mw)[2]) {
+    const uint2 pad = *reinterpret_cast<const uint2*>(m + 2 * w);
+    const uint2 by = *reinterpret_cast<const uint2*>(m + 4);
+    const unsigned long long mem = ((static_cast<unsigned long long>(by.y) << 32) | by.x) >> tb;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int col = w * 64 + q * 32;
+        const uint32_t lo = static_cast<uint32_t>(mem >> (8 * (col >> lbs))) & 1u;
+        const uint32_t hi = static_cast<uint32_t>(mem >> (8 * ((col + 16) >> lbs))) & 1u;   // another slot at bs = 16
+        mw[q] = (lo ? 0x0000FFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+        if (!all) mw[q] &= q ? pad.y : pad.x;
+    }
+}
+
 template <int D, bool KV>
 __global__ void __launch_bounds__(GRAD_THREADS, 1)
     grad_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                 const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, const GradArgs a) {
     using L = GradSmem<D>;
-    constexpr int NS = GRAD_STAGES;
+    constexpr int NS0 = GRAD_STAGES0, NS1 = GRAD_STAGES1;
     extern __shared__ __align__(1024) unsigned char smem[];
     if (smem_u32(smem) & 1023u) {   // the 128-byte swizzle needs 1024-byte aligned tiles
         if (threadIdx.x == 0) record_status(FVATTN_ERR_UNSUPPORTED);
@@ -136,7 +170,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
     const int lane = threadIdx.x & 31;
     const Geo& g = a.g;
     const int bs = g.bs;
-    const int bpc = 128 / bs;
+    const int bpc = 128 / bs, lbs = 31 - __clz(bs);
     volatile int* abort_flag = &ctl.abort_flag;
     const unsigned long long wlim = a.wait_limit_ns;
 
@@ -147,23 +181,27 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
     }
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&ctl.a_full), 1);
-        mbar_init(smem_u32(&ctl.a_empty), 1);
-        for (int s = 0; s < NS; ++s) {
+        mbar_init(smem_u32(&ctl.a_empty), 2);
+        for (int s = 0; s < NS0; ++s) {
             mbar_init(smem_u32(&ctl.b0_full[s]), 1);
-            mbar_init(smem_u32(&ctl.b0_empty[s]), 1 + 8);   // the MMAs' commit and the eight arithmetic warps
+            mbar_init(smem_u32(&ctl.b0_empty[s]), (KV ? 1 : 2) + 8);   // commits of its last products, the arithmetic warps
+        }
+        for (int s = 0; s < NS1; ++s) {
             mbar_init(smem_u32(&ctl.b1_full[s]), 1);
             mbar_init(smem_u32(&ctl.b1_empty[s]), KV ? 1 + 8 : 1);
-            mbar_init(smem_u32(&ctl.s_full[s]), 1);
+        }
+        mbar_init(smem_u32(&ctl.s_full), 1);
+        mbar_init(smem_u32(&ctl.dp_full), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&ctl.p_full[s]), 8);
             mbar_init(smem_u32(&ctl.ds_full[s]), 8);
             mbar_init(smem_u32(&ctl.item_full[s]), 1);
-            mbar_init(smem_u32(&ctl.item_empty[s]), 1 + 1 + 8);   // issuer, second producer, arithmetic
+            mbar_init(smem_u32(&ctl.item_empty[s]), 2 + 1 + 8);   // issuers, second producer, arithmetic
         }
-        mbar_init(smem_u32(&ctl.dp_full), 1);
-        mbar_init(smem_u32(&ctl.dp_free), 8);
-        mbar_init(smem_u32(&ctl.p_full), 8);
-        mbar_init(smem_u32(&ctl.acc_full), 1);
+        mbar_init(smem_u32(&ctl.sum_full), 8);
+        mbar_init(smem_u32(&ctl.acc_full), 2);
         mbar_init(smem_u32(&ctl.acc_free), 8);
-        mbar_init(smem_u32(&ctl.drain), 1);
+        for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&ctl.drain[s]), 1);
         ctl.abort_flag = 0;
         fence_mbar_init();
     }
@@ -189,6 +227,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
         const int quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const uint32_t sbuf = trow + T_S + static_cast<uint32_t>(w) * 64u;
+        const uint32_t dpbuf = trow + T_DP + static_cast<uint32_t>(w) * 64u;
         const int tb = row / bs;                    // this row's block in the tile
         const unsigned long long sl2x2 = f2_pack(a.scale_log2, a.scale_log2);
         int item_seq = 0;
@@ -210,145 +250,178 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
             const bool in_tile = row < min(a.G, g.nb - blk0) * bs;
             const long long grow = static_cast<long long>(bh) * g.Npad + static_cast<long long>(blk0) * bs + row;
             // KV: whether this key row is a token.  Else: the query row's statistics (-inf takes P to 0).
-            uint32_t row_mask = 0xFFFFFFFFu;
+            bool live = in_tile;
             unsigned long long nl2 = 0ull, nd2 = 0ull;
+            float nd = 0.f;
+            unsigned long long sum2 = 0ull;             // sum of P dP: two partial sums
+            // Padding keys are zero rows of K and V: their P, exp2(-lse2), multiplies zeros wherever it
+            // goes, and needs a mask only where it could overflow.
+            bool all = true;
             if (KV) {
                 int f_, y_, x_;
-                if (!in_tile || !token_of_pos(g, static_cast<long long>(blk0) * bs + row, f_, y_, x_)) row_mask = 0u;
+                live = live && token_of_pos(g, static_cast<long long>(blk0) * bs + row, f_, y_, x_);
             } else {
                 const float nl = in_tile ? __ldg(a.nlse2 + grow) : -INFINITY;
-                const float nd = in_tile ? __ldg(a.ndelta + grow) : 0.f;
+                if (in_tile) nd = a.ndelta[grow];
+                live = nl != -INFINITY;
                 nl2 = f2_pack(nl, nl);
                 nd2 = f2_pack(nd, nd);
-                if (nl == -INFINITY) row_mask = 0u;
+                all = __all_sync(0xffffffffu, !(nl > 60.f));
             }
             for (int i = 0; i < nc; ++i, ++c) {
-                const int st = c % NS;
-                const uint32_t sbuf = trow + T_S + (KV ? 0u : (c & 1u) * 128u) + static_cast<uint32_t>(w) * 64u;
-                const uint32_t dpbuf = trow + (KV ? T_DP_KV : T_DP_Q) + static_cast<uint32_t>(w) * 64u;
-                const uint32_t sbar = KV ? smem_u32(&ctl.s_full[0]) : smem_u32(&ctl.s_full[c & 1]);
-                const uint32_t spar = KV ? (c & 1) : ((c >> 1) & 1);
-                if (!wait_warp2(smem_u32(&ctl.b0_full[st]), (c / NS) & 1, sbar, spar, abort_flag, wlim)) {
+                const uint32_t st0 = c % NS0, st1 = c % NS1, ph = c & 1;
+                if (!wait_warp2(smem_u32(&ctl.b0_full[st0]), (c / NS0) & 1, smem_u32(&ctl.s_full), ph, abort_flag, wlim)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t mw[2];
-                mw[0] = ctl.mask[st][tb][2 * w] & row_mask;
-                mw[1] = ctl.mask[st][tb][2 * w + 1] & row_mask;
-                float p[2][32];
-                {
-                    uint32_t s0[32], s1[32];
-                    tmem_ld32(sbuf, s0);
-                    tmem_ld32(sbuf + 32u, s1);
-                    tmem_wait_ld();
-                    auto probs = [&](int h, const uint32_t (&sv)[32]) {
-                        if (mw[h] == 0u) {
+                uint32_t pv[2][32];                 // S, then P, of this row: 32 columns each
+                tmem_ld32(sbuf, pv[0]);
+                tmem_ld32(sbuf + 32u, pv[1]);
+                uint32_t mw[2];                     // columns that the row sees
+                grad_mask(ctl.mask[st0], lbs, tb, w, all, mw);
+                const bool full = __all_sync(0xffffffffu, (mw[0] & mw[1]) == 0xFFFFFFFFu);
+                tmem_wait_ld();
+                // The whole chunk's arithmetic is there twice: without masks, and with a select an element.
+                // One body that tests for masks on the way took twice the time, masks or not.
+                auto chunk = [&](auto without_masks) {
+                    constexpr bool FULL = decltype(without_masks)::value;
+                    // two bodies for the compiler too, which else moves the loads of both before the branch and spills
+                    if constexpr (FULL)
+                        asm volatile("// every column" ::: "memory");
+                    else
+                        asm volatile("// masks" ::: "memory");
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) p[h][e] = 0.f;
-                            return;
+                    for (int h = 0; h < 2; ++h) {   // P over S, for half of its product
+                        uint32_t pk[16];
+                        {
+                            const ulonglong2* nls = reinterpret_cast<const ulonglong2*>(&ctl.stat[st0][w * 64 + h * 32]);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                ulonglong2 add = make_ulonglong2(nl2, nl2);
+                                if (KV) add = nls[e >> 2];
+#pragma unroll
+                                for (int z = 0; z < 4; z += 2) {
+                                    float x0, x1;
+                                    f2_unpack(f2_fma(f2_pack(__uint_as_float(pv[h][e + z]), __uint_as_float(pv[h][e + z + 1])),
+                                                     sl2x2, z ? add.y : add.x), x0, x1);
+                                    x0 = ex2_approx(x0);
+                                    x1 = ex2_approx(x1);
+                                    if (!FULL) {
+                                        x0 = (mw[h] & (1u << (e + z))) ? x0 : 0.f;
+                                        x1 = (mw[h] & (1u << (e + z + 1))) ? x1 : 0.f;
+                                    }
+                                    pv[h][e + z] = __float_as_uint(x0);
+                                    pv[h][e + z + 1] = __float_as_uint(x1);
+                                    pk[(e + z) >> 1] = pack_bf16x2(x0, x1);
+                                }
+                            }
+                            tmem_st16(sbuf + h * 16u, pk);
                         }
-                        const unsigned long long* nls =
-                            reinterpret_cast<const unsigned long long*>(&ctl.nlse2[st][w * 64 + h * 32]);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const unsigned long long add = KV ? nls[e >> 1] : nl2;
-                            float x0, x1;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2x2, add),
-                                      x0, x1);
-                            p[h][e] = ex2_approx(x0);
-                            p[h][e + 1] = ex2_approx(x1);
-                        }
-                        if (mw[h] != 0xFFFFFFFFu) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) p[h][e] = ((mw[h] >> e) & 1u) ? p[h][e] : 0.f;
-                        }
-                    };
-                    probs(0, s0);
-                    probs(1, s1);
-                }
-                if (KV) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(p[e >> 4][(2 * e) & 31], p[e >> 4][(2 * e + 1) & 31]);
-                    tmem_st32(sbuf, pk);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_u32(&ctl.p_full));
-                        mbar_arrive(smem_u32(&ctl.b0_empty[st]));
-                    }
-                    if (!wait_warp2(smem_u32(&ctl.b1_full[st]), (c / NS) & 1, smem_u32(&ctl.dp_full), c & 1, abort_flag,
-                                    wlim)) {
-                        ok = false;
-                        break;
-                    }
-                } else {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&ctl.b0_empty[st]));
-                    if (!wait_warp(smem_u32(&ctl.dp_full), c & 1, abort_flag, wlim)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                tc_fence_after();
-                {
-                    uint32_t d0[32], d1[32], ds[32];
-                    tmem_ld32(dpbuf, d0);
-                    tmem_ld32(dpbuf + 32u, d1);
-                    tmem_wait_ld();
-                    if (!KV) {
+                        tmem_wait_st();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&ctl.dp_free));
-                    }
-                    auto grads = [&](int h, const uint32_t (&dv)[32]) {
-                        const unsigned long long* nds =
-                            reinterpret_cast<const unsigned long long*>(&ctl.ndelta[st][w * 64 + h * 32]);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const unsigned long long add = KV ? nds[e >> 1] : nd2;
-                            float x0, x1;
-                            f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), add),
-                                             f2_pack(p[h][e], p[h][e + 1])), x0, x1);
-                            // a masked pair gives 0 whatever dP holds
-                            if (mw[h] != 0xFFFFFFFFu) {
-                                x0 = ((mw[h] >> e) & 1u) ? x0 : 0.f;
-                                x1 = ((mw[h] >> (e + 1)) & 1u) ? x1 : 0.f;
-                            }
-                            ds[h * 16 + (e >> 1)] = pack_bf16x2(x0, x1);
+                        if (lane == 0) {
+                            mbar_arrive(smem_u32(&ctl.p_full[h]));
+                            if (h == 1) mbar_arrive(smem_u32(&ctl.b0_empty[st0]));
                         }
-                    };
-                    grads(0, d0);
-                    grads(1, d1);
-                    tmem_st32(KV ? dpbuf : sbuf, ds);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_u32(&ctl.ds_full[c & 1]));
-                        if (KV) mbar_arrive(smem_u32(&ctl.b1_empty[st]));
                     }
-                }
+                    if (KV) {
+                        if (!wait_warp2(smem_u32(&ctl.b1_full[st1]), (c / NS1) & 1, smem_u32(&ctl.dp_full), ph,
+                                        abort_flag, wlim))
+                            return false;
+                    } else if (!wait_warp(smem_u32(&ctl.dp_full), ph, abort_flag, wlim)) {
+                        return false;
+                    }
+                    tc_fence_after();
+                    uint32_t dv[2][32];
+                    tmem_ld32(dpbuf, dv[0]);
+                    tmem_ld32(dpbuf + 32u, dv[1]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t ds[16];
+                        {
+                            // (the bits' tests are made again: kept from above they would take 64 registers)
+                            if (!FULL) asm volatile("" : "+r"(mw[h]));
+                            const ulonglong2* nds = reinterpret_cast<const ulonglong2*>(&ctl.stat[NS0 + st1][w * 64 + h * 32]);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                ulonglong2 add = make_ulonglong2(nd2, nd2);
+                                if (KV) add = nds[e >> 2];
+#pragma unroll
+                                for (int z = 0; z < 4; z += 2) {
+                                    float x0 = __uint_as_float(dv[h][e + z]), x1 = __uint_as_float(dv[h][e + z + 1]);
+                                    if (!FULL && !KV) {   // nothing of a masked pair enters the sum
+                                        x0 = (mw[h] & (1u << (e + z))) ? x0 : 0.f;
+                                        x1 = (mw[h] & (1u << (e + z + 1))) ? x1 : 0.f;
+                                    }
+                                    const unsigned long long dp2 = f2_pack(x0, x1);
+                                    const unsigned long long p2 =
+                                        f2_pack(__uint_as_float(pv[h][e + z]), __uint_as_float(pv[h][e + z + 1]));
+                                    if (!KV) sum2 = f2_fma(p2, dp2, sum2);
+                                    f2_unpack(f2_mul(f2_add(dp2, z ? add.y : add.x), p2), x0, x1);
+                                    if (!FULL && KV) {    // 0 whatever dP and the column's statistics hold
+                                        x0 = (mw[h] & (1u << (e + z))) ? x0 : 0.f;
+                                        x1 = (mw[h] & (1u << (e + z + 1))) ? x1 : 0.f;
+                                    }
+                                    ds[(e + z) >> 1] = pack_bf16x2(x0, x1);
+                                }
+                            }
+                            tmem_st16(dpbuf + h * 16u, ds);   // its columns' dP has been read
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(smem_u32(&ctl.ds_full[h]));
+                            if (KV && h == 1) mbar_arrive(smem_u32(&ctl.b1_empty[st1]));
+                        }
+                    }
+                    return true;
+                };
+                ok = full ? chunk(std::true_type{}) : chunk(std::false_type{});
+                if (!ok) break;
             }
             if (!ok) break;
-            // ---- epilogue.  KV: group 0 writes dV, group 1 dK; else each writes half of dQ's columns.
+            // ---- epilogue.  KV: columns' half 0 writes dV, 1 dK; else each writes half of dQ's columns.
+            float fix = 0.f;     // delta0 - delta
             if (nc > 0) {
+                if (!KV) {
+                    float s0, s1;
+                    f2_unpack(sum2, s0, s1);
+                    float* sums = ctl.stat[(n_seq & 1) * 2];   // the item before may still be read
+                    sums[w * 128 + row] = s0 + s1;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&ctl.sum_full));
+                    if (!wait_warp(smem_u32(&ctl.sum_full), n_seq & 1, abort_flag, wlim)) break;
+                    const float nd1 = -(sums[row] + sums[128 + row]);
+                    fix = nd1 - nd;
+                    if (live && w == 0) a.ndelta[grow] = nd1;
+                }
                 if (!wait_warp(smem_u32(&ctl.acc_full), n_seq & 1, abort_flag, wlim)) break;
                 tc_fence_after();
             }
-            const float f = KV ? (w == 0 ? 1.f : a.scale) : a.scale;
+            const float f = KV && w == 0 ? 1.f : a.scale;
             __nv_bfloat16* dst = (KV && w == 1 ? a.out1 : a.out0) + grow * D;
-            const uint32_t acc = trow + (KV ? (w == 0 ? T_DV : T_DK) : T_DQ);
+            const uint32_t acc = trow + (KV && w == 0 ? T_A0 : T_A1);
             constexpr int NQ = KV ? D / 32 : D / 64;
 #pragma unroll 1
             for (int q = 0; q < NQ; ++q) {
                 const uint32_t col = (KV ? 0u : static_cast<uint32_t>(w) * (D / 2)) + q * 32u;
                 uint32_t r[32];
-                if (nc > 0) {
+                if (nc > 0) {   // (rows that take no part may hold anything: they get zero)
                     tmem_ld32(acc + col, r);
-                    tmem_wait_ld();
+                    if (!KV) {
+                        uint32_t pk[32];
+                        tmem_ld32(trow + T_A0 + col, pk);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            r[e] = __float_as_uint(fmaf(fix, __uint_as_float(pk[e]), __uint_as_float(r[e])));
+                    } else {
+                        tmem_wait_ld();
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) r[e] = 0u;
@@ -359,8 +432,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                         uint32_t o[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            o[k] = pack_bf16x2(__uint_as_float(r[v8 * 8 + 2 * k]) * f,
-                                               __uint_as_float(r[v8 * 8 + 2 * k + 1]) * f);
+                            o[k] = live ? pack_bf16x2(__uint_as_float(r[v8 * 8 + 2 * k]) * f,
+                                                      __uint_as_float(r[v8 * 8 + 2 * k + 1]) * f)
+                                        : 0u;
                         *reinterpret_cast<uint4*>(dst + col + v8 * 8) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
                 }
@@ -434,33 +508,30 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 }
                 const uint32_t* ul = a.ul + unit * g.nb;
                 for (int i = 0; i < nc; ++i, ++c) {
-                    const int st = c % NS;
+                    const int st = c % NS0;
                     uint32_t mem = 0u;
                     const int j = lane < bpc ? grad_slot(ul, i * bpc + lane, cnt, mem) : -1;
                     const int ext = !KV && j >= 0 ? __ldg(a.ext + j) : 0;
-                    if (!wait_warp(smem_u32(&ctl.b0_empty[st]), ((c / NS) & 1) ^ 1, abort_flag, wlim)) {
+                    if (!wait_warp(smem_u32(&ctl.b0_empty[st]), ((c / NS0) & 1) ^ 1, abort_flag, wlim)) {
                         ok = false;
                         break;
                     }
-                    // columns a row of the tile's block tq sees: the slot's block is paired with tq, and
-                    // (for keys) the column is a token.  Query rows take no part through their statistics.
-                    uint32_t pad[4], mq[4];
+                    // columns that are tokens (query rows take no part through their statistics), and which
+                    // blocks of the tile each slot's block is paired with
+                    uint32_t pad[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int e = __shfl_sync(0xffffffffu, ext, c_slot[q]);
-                        mq[q] = __shfl_sync(0xffffffffu, mem, c_slot[q]);
                         pad[q] = KV ? 0xFFFFFFFFu
                                     : __ballot_sync(0xffffffffu, (c_of[q] < (e & 255)) && (c_oy[q] < ((e >> 8) & 255)) &&
                                                                      (c_ox[q] < (e >> 16)));
                     }
-                    for (int tq = 0; tq < a.G; ++tq) {
-                        uint32_t words[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) words[q] = pad[q] & __ballot_sync(0xffffffffu, (mq[q] >> tq) & 1u);
-                        if (lane == 0) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) ctl.mask[st][tq][q] = words[q];
-                        }
+                    const uint32_t byte = mem << (8 * (lane & 3));
+                    const uint32_t m0 = __reduce_or_sync(0xffffffffu, lane < 4 ? byte : 0u);
+                    const uint32_t m1 = __reduce_or_sync(0xffffffffu, lane >= 4 && lane < 8 ? byte : 0u);
+                    if (lane == 0) {
+                        *reinterpret_cast<uint4*>(&ctl.mask[st][0]) = make_uint4(pad[0], pad[1], pad[2], pad[3]);
+                        *reinterpret_cast<uint2*>(&ctl.mask[st][4]) = make_uint2(m0, m1);
                     }
                     const uint32_t bar = smem_u32(&ctl.b0_full[st]);
                     const int nblk = min(bpc, cnt - i * bpc);
@@ -475,14 +546,14 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
 #pragma unroll
                         for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + h * 16384u, &tmB0, h * 64, r, bar);
                         if (KV && j >= 0)
-                            bulk_load(smem_u32(&ctl.nlse2[st][lane * bs]), a.nlse2 + r, static_cast<uint32_t>(bs * 4), bar);
+                            bulk_load(smem_u32(&ctl.stat[st][lane * bs]), a.nlse2 + r, static_cast<uint32_t>(bs * 4), bar);
                     }
                 }
             }
             if (lane == 0) {   // no copy into shared memory outlives the CTA
                 if (n_seq > 0) wait_bar_drain(smem_u32(&ctl.a_full), (n_seq - 1) & 1, wlim);
-                for (int st = 0; st < NS; ++st) {
-                    const uint32_t fills = c > static_cast<uint32_t>(st) ? (c - st + NS - 1) / NS : 0u;
+                for (int st = 0; st < NS0; ++st) {
+                    const uint32_t fills = c > static_cast<uint32_t>(st) ? (c - st + NS0 - 1) / NS0 : 0u;
                     if (fills > 0) wait_bar_drain(smem_u32(&ctl.b0_full[st]), (fills - 1) & 1, wlim);
                 }
             }
@@ -507,10 +578,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 const int row_base = bh * static_cast<int>(g.Npad);
                 const uint32_t* ul = a.ul + (static_cast<long long>(bh) * a.ngroups + u) * g.nb;
                 for (int i = 0; i < nc; ++i, ++c) {
-                    const int st = c % NS;
+                    const int st = c % NS1;
                     uint32_t mem = 0u;
                     const int j = lane < bpc ? grad_slot(ul, i * bpc + lane, cnt, mem) : -1;
-                    if (!wait_warp(smem_u32(&ctl.b1_empty[st]), ((c / NS) & 1) ^ 1, abort_flag, wlim)) {
+                    if (!wait_warp(smem_u32(&ctl.b1_empty[st]), ((c / NS1) & 1) ^ 1, abort_flag, wlim)) {
                         ok = false;
                         break;
                     }
@@ -525,47 +596,60 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
 #pragma unroll
                         for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + h * 16384u, &tmB1, h * 64, r, bar);
                         if (KV && j >= 0)
-                            bulk_load(smem_u32(&ctl.ndelta[st][lane * bs]), a.ndelta + r, static_cast<uint32_t>(bs * 4), bar);
+                            bulk_load(smem_u32(&ctl.stat[NS0 + st][lane * bs]), a.ndelta + r, static_cast<uint32_t>(bs * 4), bar);
                     }
                 }
             }
             if (lane == 0) {
-                for (int st = 0; st < NS; ++st) {
-                    const uint32_t fills = c > static_cast<uint32_t>(st) ? (c - st + NS - 1) / NS : 0u;
+                for (int st = 0; st < NS1; ++st) {
+                    const uint32_t fills = c > static_cast<uint32_t>(st) ? (c - st + NS1 - 1) / NS1 : 0u;
                     if (fills > 0) wait_bar_drain(smem_u32(&ctl.b1_full[st]), (fills - 1) & 1, wlim);
                 }
             }
             __syncwarp();
-        } else if (warp == 1) {
-            // =========================== MMA issuer (one lane)
+        } else {
+            // =========================== MMA issuers (one lane each of warps 1 and 3)
+            // Warp 1: A0 += P(i-1) B, S(i).  Warp 3: A1 += dS(i-1) B0, dP(i).  In each the second product
+            // overwrites columns that the first reads: one thread's MMAs keep their order.  While one
+            // thread waits on its barriers the other's MMAs run; with a single issuer the pipe ran dry at
+            // every wait (4200 clocks a chunk where its four products take 2048).
             if (lane == 0) {
                 constexpr uint32_t ID_SS = idesc_bf16_f32(128, 128, false);
                 constexpr uint32_t ID_ACC = idesc_bf16_f32(128, D, true);
+                // A descriptor's upper half is one constant for all operands and the lower half holds the
+                // address: one add an operand.
+                constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);
                 // C = own tile (A, K-major) x streamed chunk (B, K-major)
                 auto product = [&](uint32_t d, uint32_t abase, uint32_t bbase) {
+                    abase = (abase >> 4) | (1u << 16);
+                    bbase = (bbase >> 4) | (1u << 16);
+                    asm volatile("" : "+r"(abase), "+r"(bbase));   // (not kept for every step: they would spill)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * 16384u + (kk & 3) * 32u;
-                        mma_bf16_ss(d, sw128_desc(abase + off, 16u, 1024u), sw128_desc(bbase + off, 16u, 1024u), ID_SS,
-                                    kk > 0 ? 1u : 0u);
+                        const uint32_t off = ((kk >> 2) * 16384u + (kk & 3) * 32u) >> 4;
+                        mma_bf16_ss(d, desc_of(abase + off, HI), desc_of(bbase + off, HI), ID_SS, kk > 0 ? 1u : 0u);
                     }
                 };
                 // acc += A (bf16 in tensor memory, 64 columns of K in each of two 64-column halves) x chunk
-                // (B, its 128 rows are K)
-                auto accumulate = [&](uint32_t d, uint32_t abuf, uint32_t bbase, bool first) {
+                // (B, its 128 rows are K), the steps of one 32-column piece of each half
+                auto accumulate = [&](uint32_t d, uint32_t abuf, uint32_t bbase, uint32_t piece, bool first) {
+                    bbase = (bbase >> 4) | ((16384u >> 4) << 16);
+                    asm volatile("" : "+r"(bbase));
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ts(d, abuf + (kk >> 2) * 64u + (kk & 3) * 8u, sw128_desc(bbase + kk * 2048u, 16384u, 1024u),
-                                    ID_ACC, (first && kk == 0) ? 0u : 1u);
+                    for (uint32_t z = 0; z < 4; ++z) {
+                        const uint32_t in = piece * 2u + (z & 1u), half = z >> 1;   // step of the half
+                        mma_bf16_ts(d, abuf + half * 64u + in * 8u, desc_of(bbase + (((half * 4u + in) * 2048u) >> 4), HI),
+                                    ID_ACC, (z > 0 || !first) ? 1u : 0u);
+                    }
                 };
-                const uint32_t sA0 = sbase + L::A0, sA1 = sbase + L::A1, sB0 = sbase + L::B0, sB1 = sbase + L::B1;
-                int item_seq = 0;
-                uint32_t n_seq = 0, c0 = 0;
                 bool ok = true;
                 auto need = [&](uint32_t bar, uint32_t parity) {
                     if (ok) ok = wait_bar(bar, parity, abort_flag, wlim);
                     return ok;
                 };
+                int item_seq = 0;
+                uint32_t n_seq = 0, c = 0;
+                const bool first_role = warp == 1;
                 while (ok) {
                     const int slot = item_seq & 1;
                     if (!need(smem_u32(&ctl.item_full[slot]), (item_seq >> 1) & 1)) break;
@@ -577,68 +661,62 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                     const int nc = (cnt + bpc - 1) / bpc;
                     if (nc == 0) continue;
                     if (!need(smem_u32(&ctl.a_full), n_seq & 1)) break;
-                    for (int i = 0; i <= nc; ++i) {
-                        const uint32_t c = c0 + i;
-                        const int st = c % NS;
-                        const uint32_t ph = (c / NS) & 1;
-                        if (i < nc) {
-                            // S: its buffer was last read by an accumulating product issued before
-                            if (!need(smem_u32(&ctl.b0_full[st]), ph)) break;
+                    if (first_role) {
+                        for (int i = 0; i <= nc; ++i, ++c) {
+                            const uint32_t cp = c - 1;
+                            const uint32_t st0 = c % NS0, sp = cp % (KV ? NS1 : NS0);
+                            if (i < nc && !need(smem_u32(&ctl.b0_full[st0]), (c / NS0) & 1)) break;
+                            if (i > 0) {
+                                if (i == 1 && !need(smem_u32(&ctl.acc_free), (n_seq & 1) ^ 1)) break;
+                                if (KV && !need(smem_u32(&ctl.b1_full[sp]), (cp / NS1) & 1)) break;
+                                const uint32_t b = sbase + (KV ? L::B1 : L::B0) + sp * L::TILE;
+#pragma unroll
+                                for (uint32_t half = 0; half < 2; ++half) {
+                                    if (!need(smem_u32(&ctl.p_full[half]), cp & 1)) break;
+                                    tc_fence_after();
+                                    accumulate(tmem + T_A0, tmem + T_S, b, half, half == 0 && i == 1);
+                                }
+                                if (!ok) break;
+                                mma_commit(smem_u32(KV ? &ctl.b1_empty[sp] : &ctl.b0_empty[sp]));
+                            }
+                            if (i == nc) break;
                             tc_fence_after();
-                            product(tmem + T_S + (KV ? 0u : (c & 1u) * 128u), sA0, sB0 + st * L::TILE);
-                            mma_commit(smem_u32(&ctl.s_full[KV ? 0 : (c & 1)]));
+                            product(tmem + T_S, sbase + L::A0, sbase + L::B0 + st0 * L::TILE);
+                            mma_commit(smem_u32(&ctl.s_full));
+                            if (i == nc - 1) mma_commit(smem_u32(&ctl.a_empty));
                         }
-                        if (KV) {
-                            if (i > 0) {   // dK += dS^T Q of the chunk before
-                                const int sp = (c - 1) % NS;
-                                if (!need(smem_u32(&ctl.ds_full[(c - 1) & 1]), ((c - 1) >> 1) & 1)) break;
+                    } else {
+                        for (int i = 0; i <= nc; ++i, ++c) {
+                            const uint32_t cp = c - 1;
+                            const uint32_t st1 = c % NS1, sp = cp % NS0;
+                            if (i < nc && !need(smem_u32(&ctl.b1_full[st1]), (c / NS1) & 1)) break;
+                            if (i > 0) {
                                 if (i == 1 && !need(smem_u32(&ctl.acc_free), (n_seq & 1) ^ 1)) break;
-                                tc_fence_after();
-                                accumulate(tmem + T_DK, tmem + T_DP_KV, sB0 + sp * L::TILE, i == 1);
+                                if (!need(smem_u32(&ctl.b0_full[sp]), (cp / NS0) & 1)) break;
+#pragma unroll
+                                for (uint32_t half = 0; half < 2; ++half) {
+                                    if (!need(smem_u32(&ctl.ds_full[half]), cp & 1)) break;
+                                    tc_fence_after();
+                                    accumulate(tmem + T_A1, tmem + T_DP, sbase + L::B0 + sp * L::TILE, half, half == 0 && i == 1);
+                                }
+                                if (!ok) break;
                                 mma_commit(smem_u32(&ctl.b0_empty[sp]));
                             }
-                            if (i < nc) {
-                                if (!need(smem_u32(&ctl.b1_full[st]), ph)) break;
-                                tc_fence_after();
-                                product(tmem + T_DP_KV, sA1, sB1 + st * L::TILE);
-                                mma_commit(smem_u32(&ctl.dp_full));
-                                if (i == nc - 1) mma_commit(smem_u32(&ctl.a_empty));
-                                if (!need(smem_u32(&ctl.p_full), c & 1)) break;
-                                if (i == 0 && !need(smem_u32(&ctl.acc_free), (n_seq & 1) ^ 1)) break;
-                                tc_fence_after();
-                                accumulate(tmem + T_DV, tmem + T_S, sB1 + st * L::TILE, i == 0);
-                                mma_commit(smem_u32(&ctl.b1_empty[st]));
-                            }
-                        } else {
-                            if (i < nc) {
-                                // dP: the arithmetic has read the chunk before's
-                                if (!need(smem_u32(&ctl.b1_full[st]), ph)) break;
-                                if (c > 0 && !need(smem_u32(&ctl.dp_free), (c - 1) & 1)) break;
-                                tc_fence_after();
-                                product(tmem + T_DP_Q, sA1, sB1 + st * L::TILE);
-                                mma_commit(smem_u32(&ctl.dp_full));
-                                mma_commit(smem_u32(&ctl.b1_empty[st]));
-                                if (i == nc - 1) mma_commit(smem_u32(&ctl.a_empty));
-                            }
-                            if (i > 0) {   // dQ += dS K of the chunk before
-                                const uint32_t cp = c - 1;
-                                const int sp = cp % NS;
-                                if (!need(smem_u32(&ctl.ds_full[cp & 1]), (cp >> 1) & 1)) break;
-                                if (i == 1 && !need(smem_u32(&ctl.acc_free), (n_seq & 1) ^ 1)) break;
-                                tc_fence_after();
-                                accumulate(tmem + T_DQ, tmem + T_S + (cp & 1u) * 128u, sB0 + sp * L::TILE, i == 1);
-                                mma_commit(smem_u32(&ctl.b0_empty[sp]));
-                            }
+                            if (i == nc) break;
+                            tc_fence_after();
+                            product(tmem + T_DP, sbase + L::A1, sbase + L::B1 + st1 * L::TILE);
+                            mma_commit(smem_u32(&ctl.dp_full));
+                            if (!KV) mma_commit(smem_u32(&ctl.b1_empty[st1]));
+                            if (i == nc - 1) mma_commit(smem_u32(&ctl.a_empty));
                         }
                     }
                     if (!ok) break;
                     mma_commit(smem_u32(&ctl.acc_full));
-                    c0 += nc;
                     ++n_seq;
                 }
-                // every MMA issued has completed before the tensor memory is released
-                mma_commit(smem_u32(&ctl.drain));
-                wait_bar_drain(smem_u32(&ctl.drain), 0, wlim);
+                // every MMA this thread issued has completed before the tensor memory is released
+                mma_commit(smem_u32(&ctl.drain[warp >> 1]));
+                wait_bar_drain(smem_u32(&ctl.drain[warp >> 1]), 0, wlim);
             }
             __syncwarp();
         }
@@ -932,21 +1010,21 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
     a.oob_row = static_cast<int>(rows);
     a.wait_limit_ns = WAIT_LIMIT_NS;
     const int grid = nsm < a.total_items ? nsm : a.total_items;
-    a.ul = ulk;
-    a.cnt = cntk;
-    a.order = ordk;
-    a.counter = counters + 1;
-    a.out0 = static_cast<__nv_bfloat16*>(dv_t);
-    a.out1 = static_cast<__nv_bfloat16*>(dk_t);
-    int rc = launch_grad<D, true>(tk, tv, tq, tdo, a, grid, s);
-    if (rc != FVATTN_OK) return rc;
     a.ul = ulq;
     a.cnt = cntq;
     a.order = ordq;
     a.counter = counters;
     a.out0 = static_cast<__nv_bfloat16*>(dq_t);
     a.out1 = nullptr;
-    return launch_grad<D, false>(tq, tdo, tk, tv, a, grid, s);
+    int rc = launch_grad<D, false>(tq, tdo, tk, tv, a, grid, s);
+    if (rc != FVATTN_OK) return rc;
+    a.ul = ulk;
+    a.cnt = cntk;
+    a.order = ordk;
+    a.counter = counters + 1;
+    a.out0 = static_cast<__nv_bfloat16*>(dv_t);
+    a.out1 = static_cast<__nv_bfloat16*>(dk_t);
+    return launch_grad<D, true>(tk, tv, tq, tdo, a, grid, s);
 }
 
 }  // namespace fv
