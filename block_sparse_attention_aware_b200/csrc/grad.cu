@@ -15,11 +15,16 @@
 //
 // delta.  dP - delta cancels where a softmax is concentrated, and dO . O from
 // the bf16 O is then too coarse: with scores of standard deviation 3 the
-// gradients' error against 64 bits was 1.7 times that of rounding the result.
-// The query pass therefore starts from delta0 = dO . O and sums the exact
-// delta_t = sum_u P_tu dP_tu on the way; its dQ is put right at the end,
+// gradients' error against 64 bits was 1.7 times that of rounding the result
+// (1.41 is the rounding of dS and the result).  The query pass therefore
+// starts from delta0 = dO . O and sums the exact delta_t = sum_u P_tu dP_tu
+// on the way, which the key pass reads.  Its own dQ is put right at the end,
 //   dQ = scale (sum_u dS0_tu k_u - (delta - delta0) sum_u P_tu k_u),
-// for a product more, and the key pass reads the exact delta.
+// with a product more, in the tiles that need it.  delta0's error is about
+// 2^-9 |dO| |O| / sqrt(3 D) and dP - delta varies by |dO| |v| / sqrt(D), so
+// that it adds |O| / |v| roundings to the result: tiles with a row of
+// |O|^2 > GRAD_EXACT mean |v|^2 take the product (1/16: an error of at most
+// sqrt(2 + 1/16) = 1.44 roundings in the others).
 //
 // Both passes are one kernel, grad_kernel<D, KV>, one CTA of 384 threads per
 // SM (it holds all 512 tensor-memory columns):
@@ -38,7 +43,9 @@
 // with the stream.  Else rows are queries with their statistics in registers.
 // Per chunk i, in tensor memory (all 512 columns):
 //   S(i) -> P(i) over it, A0 += P(i) B;   dP(i) -> dS(i) over it, A1 += dS(i) B0
-// with KV: A0 = dV (B = dO), A1 = dK; else A0 = sum P k (B = B0), A1 = dQ.
+// with KV: A0 = dV (B = dO), A1 = dK; else A0 = sum P k (B = B0), A1 = dQ.  A
+// query tile without A0 has a second dP buffer in its place, and S(i + 1) and
+// dP(i + 1) run ahead of the arithmetic.
 //
 // bs < 128: as in the forward, a tile holds G = 128 / bs consecutive blocks
 // and walks the union of their lists; a chunk packs 128 / bs listed blocks and
@@ -60,6 +67,8 @@ constexpr int GRAD_THREADS = 384;
 // over one and a half chunks' time: a stage more.
 constexpr int GRAD_STAGES0 = 3, GRAD_STAGES1 = 2;
 constexpr uint32_t GRAD_TMEM = 512;
+constexpr float GRAD_EXACT = 1.f / 16.f;
+constexpr int GRAD_FLAG = 1 << 30;   // in the work order: a query tile that needs the exact delta
 constexpr int GRAD_GROUP = 8;     // blocks per tile at bs = 16
 // Register split (setmaxnreg): the launch gives 168 a thread; one warpgroup
 // of producers and issuer at LOW, two of arithmetic at HIGH.
@@ -74,7 +83,7 @@ struct GradArgs {
     int G, ngroups;
     const uint32_t* ul;       // [B*H][ngroups][nb] this pass's lists: block | membership bits << 24
     const int32_t* cnt;       // [B*H][ngroups] their lengths
-    const int32_t* order;     // [B*H][ngroups] tiles of a head, longest first
+    const int32_t* order;     // [B*H][ngroups] tiles of a head, longest first; with GRAD_FLAG
     int* counter;
     const int32_t* ext;       // [nb] real extent of each block
     const float* nlse2;       // [B*H][Npad] -lse * log2(e); -inf for rows that take no part
@@ -96,12 +105,13 @@ struct __align__(16) GradCtrl {
     unsigned long long a_full, a_empty;                          // the item's own tile pair
     unsigned long long b0_full[GRAD_STAGES0], b0_empty[GRAD_STAGES0];
     unsigned long long b1_full[GRAD_STAGES1], b1_empty[GRAD_STAGES1];
-    unsigned long long s_full, dp_full, p_full[2], ds_full[2];
+    unsigned long long s_full[2], dp_full[2], ds_full[2];        // by the chunk's parity: their waiters may lag by one
+    unsigned long long p_full[2];                                // by the piece; without A0 both say that S has been read
     unsigned long long sum_full;
     unsigned long long acc_full, acc_free;
     unsigned long long item_full[2], item_empty[2];
     unsigned long long drain[2];
-    int item[2][4];            // bh, tile, list length, valid
+    int item[2][4];            // bh, tile, list length, 0: end, 1: without A0, 2: with A0
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -190,9 +200,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
             mbar_init(smem_u32(&ctl.b1_full[s]), 1);
             mbar_init(smem_u32(&ctl.b1_empty[s]), KV ? 1 + 8 : 1);
         }
-        mbar_init(smem_u32(&ctl.s_full), 1);
-        mbar_init(smem_u32(&ctl.dp_full), 1);
         for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&ctl.s_full[s]), 1);
+            mbar_init(smem_u32(&ctl.dp_full[s]), 1);
             mbar_init(smem_u32(&ctl.p_full[s]), 8);
             mbar_init(smem_u32(&ctl.ds_full[s]), 8);
             mbar_init(smem_u32(&ctl.item_full[s]), 1);
@@ -228,7 +238,6 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
         const int row = quad * 32 + lane;
         const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const uint32_t sbuf = trow + T_S + static_cast<uint32_t>(w) * 64u;
-        const uint32_t dpbuf = trow + T_DP + static_cast<uint32_t>(w) * 64u;
         const int tb = row / bs;                    // this row's block in the tile
         const unsigned long long sl2x2 = f2_pack(a.scale_log2, a.scale_log2);
         int item_seq = 0;
@@ -241,10 +250,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
             const int bh = ctl.item[slot][0];
             const int u = ctl.item[slot][1];
             const int cnt = ctl.item[slot][2];
-            const int valid = ctl.item[slot][3];
+            const int kind = ctl.item[slot][3];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl.item_empty[slot]));
-            if (!valid) break;
+            if (!kind) break;
+            const bool two = KV || kind == 2;
             const int nc = (cnt + bpc - 1) / bpc;
             const int blk0 = u * a.G;
             const bool in_tile = row < min(a.G, g.nb - blk0) * bs;
@@ -269,8 +279,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 all = __all_sync(0xffffffffu, !(nl > 60.f));
             }
             for (int i = 0; i < nc; ++i, ++c) {
-                const uint32_t st0 = c % NS0, st1 = c % NS1, ph = c & 1;
-                if (!wait_warp2(smem_u32(&ctl.b0_full[st0]), (c / NS0) & 1, smem_u32(&ctl.s_full), ph, abort_flag, wlim)) {
+                const uint32_t st0 = c % NS0, st1 = c % NS1, par = c & 1, ph = (c >> 1) & 1;
+                const uint32_t dpbuf = trow + (!two && (i & 1) ? T_A0 : T_DP) + static_cast<uint32_t>(w) * 64u;
+                if (!wait_warp2(smem_u32(&ctl.b0_full[st0]), (c / NS0) & 1, smem_u32(&ctl.s_full[par]), ph, abort_flag,
+                                wlim)) {
                     ok = false;
                     break;
                 }
@@ -284,13 +296,22 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 tmem_wait_ld();
                 // The whole chunk's arithmetic is there twice: without masks, and with a select an element.
                 // One body that tests for masks on the way took twice the time, masks or not.
-                auto chunk = [&](auto without_masks) {
-                    constexpr bool FULL = decltype(without_masks)::value;
-                    // two bodies for the compiler too, which else moves the loads of both before the branch and spills
+                auto chunk = [&](auto without_masks, auto with_a0) {
+                    constexpr bool FULL = decltype(without_masks)::value, TWO = decltype(with_a0)::value;
+                    // several bodies for the compiler too, which else moves the loads of all before the branch
                     if constexpr (FULL)
                         asm volatile("// every column" ::: "memory");
                     else
                         asm volatile("// masks" ::: "memory");
+                    if constexpr (!TWO) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(smem_u32(&ctl.p_full[0]));
+                            mbar_arrive(smem_u32(&ctl.p_full[1]));
+                            mbar_arrive(smem_u32(&ctl.b0_empty[st0]));
+                        }
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {   // P over S, for half of its product
                         uint32_t pk[16];
@@ -313,24 +334,26 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                                     }
                                     pv[h][e + z] = __float_as_uint(x0);
                                     pv[h][e + z + 1] = __float_as_uint(x1);
-                                    pk[(e + z) >> 1] = pack_bf16x2(x0, x1);
+                                    if (TWO) pk[(e + z) >> 1] = pack_bf16x2(x0, x1);
                                 }
                             }
-                            tmem_st16(sbuf + h * 16u, pk);
                         }
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(smem_u32(&ctl.p_full[h]));
-                            if (h == 1) mbar_arrive(smem_u32(&ctl.b0_empty[st0]));
+                        if constexpr (TWO) {
+                            tmem_st16(sbuf + h * 16u, pk);
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(smem_u32(&ctl.p_full[h]));
+                                if (h == 1) mbar_arrive(smem_u32(&ctl.b0_empty[st0]));
+                            }
                         }
                     }
                     if (KV) {
-                        if (!wait_warp2(smem_u32(&ctl.b1_full[st1]), (c / NS1) & 1, smem_u32(&ctl.dp_full), ph,
+                        if (!wait_warp2(smem_u32(&ctl.b1_full[st1]), (c / NS1) & 1, smem_u32(&ctl.dp_full[par]), ph,
                                         abort_flag, wlim))
                             return false;
-                    } else if (!wait_warp(smem_u32(&ctl.dp_full), ph, abort_flag, wlim)) {
+                    } else if (!wait_warp(smem_u32(&ctl.dp_full[par]), ph, abort_flag, wlim)) {
                         return false;
                     }
                     tc_fence_after();
@@ -368,19 +391,22 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                                     ds[(e + z) >> 1] = pack_bf16x2(x0, x1);
                                 }
                             }
-                            tmem_st16(dpbuf + h * 16u, ds);   // its columns' dP has been read
                         }
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(smem_u32(&ctl.ds_full[h]));
-                            if (KV && h == 1) mbar_arrive(smem_u32(&ctl.b1_empty[st1]));
-                        }
+                        tmem_st16(dpbuf + h * 16u, ds);   // (all of dP has been read)
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&ctl.ds_full[par]));
+                        if (KV) mbar_arrive(smem_u32(&ctl.b1_empty[st1]));
                     }
                     return true;
                 };
-                ok = full ? chunk(std::true_type{}) : chunk(std::false_type{});
+                if (two)
+                    ok = full ? chunk(std::true_type{}, std::true_type{}) : chunk(std::false_type{}, std::true_type{});
+                else if constexpr (!KV)
+                    ok = full ? chunk(std::true_type{}, std::false_type{}) : chunk(std::false_type{}, std::false_type{});
                 if (!ok) break;
             }
             if (!ok) break;
@@ -412,7 +438,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 uint32_t r[32];
                 if (nc > 0) {   // (rows that take no part may hold anything: they get zero)
                     tmem_ld32(acc + col, r);
-                    if (!KV) {
+                    if (!KV && two) {
                         uint32_t pk[32];
                         tmem_ld32(trow + T_A0 + col, pk);
                         tmem_wait_ld();
@@ -478,14 +504,15 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                     break;
                 }
                 const int bh = t / a.ngroups;
-                const int u = __ldg(a.order + t);
+                const int entry = __ldg(a.order + t);
+                const int u = entry & (GRAD_FLAG - 1);
                 const long long unit = static_cast<long long>(bh) * a.ngroups + u;
                 const int cnt = __ldg(a.cnt + unit);
                 if (lane == 0) {
                     ctl.item[slot][0] = bh;
                     ctl.item[slot][1] = u;
                     ctl.item[slot][2] = cnt;
-                    ctl.item[slot][3] = 1;
+                    ctl.item[slot][3] = KV || (entry & GRAD_FLAG) ? 2 : 1;
                     mbar_arrive(smem_u32(&ctl.item_full[slot]));
                 }
                 ++item_seq;
@@ -612,7 +639,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
             // Warp 1: A0 += P(i-1) B, S(i).  Warp 3: A1 += dS(i-1) B0, dP(i).  In each the second product
             // overwrites columns that the first reads: one thread's MMAs keep their order.  While one
             // thread waits on its barriers the other's MMAs run; with a single issuer the pipe ran dry at
-            // every wait (4200 clocks a chunk where its four products take 2048).
+            // every wait (4200 clocks a chunk where its four products take 2048).  The exponentials wait for
+            // A0 and S only, so warp 3 holds its products back until S(i) is done: 3400 to 3000 clocks.
             if (lane == 0) {
                 constexpr uint32_t ID_SS = idesc_bf16_f32(128, 128, false);
                 constexpr uint32_t ID_ACC = idesc_bf16_f32(128, D, true);
@@ -631,7 +659,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                     }
                 };
                 // acc += A (bf16 in tensor memory, 64 columns of K in each of two 64-column halves) x chunk
-                // (B, its 128 rows are K), the steps of one 32-column piece of each half
+                // (B, its 128 rows are K): the steps of one 32-column piece of each half
                 auto accumulate = [&](uint32_t d, uint32_t abuf, uint32_t bbase, uint32_t piece, bool first) {
                     bbase = (bbase >> 4) | ((16384u >> 4) << 16);
                     asm volatile("" : "+r"(bbase));
@@ -653,10 +681,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 while (ok) {
                     const int slot = item_seq & 1;
                     if (!need(smem_u32(&ctl.item_full[slot]), (item_seq >> 1) & 1)) break;
-                    const int valid = ctl.item[slot][3];
+                    const int kind = ctl.item[slot][3];
                     const int cnt = ctl.item[slot][2];
                     mbar_arrive(smem_u32(&ctl.item_empty[slot]));
-                    if (!valid) break;
+                    if (!kind) break;
+                    const bool two = KV || kind == 2;
                     ++item_seq;
                     const int nc = (cnt + bpc - 1) / bpc;
                     if (nc == 0) continue;
@@ -666,23 +695,26 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                             const uint32_t cp = c - 1;
                             const uint32_t st0 = c % NS0, sp = cp % (KV ? NS1 : NS0);
                             if (i < nc && !need(smem_u32(&ctl.b0_full[st0]), (c / NS0) & 1)) break;
-                            if (i > 0) {
+                            if (two && i > 0) {
                                 if (i == 1 && !need(smem_u32(&ctl.acc_free), (n_seq & 1) ^ 1)) break;
                                 if (KV && !need(smem_u32(&ctl.b1_full[sp]), (cp / NS1) & 1)) break;
                                 const uint32_t b = sbase + (KV ? L::B1 : L::B0) + sp * L::TILE;
 #pragma unroll
-                                for (uint32_t half = 0; half < 2; ++half) {
-                                    if (!need(smem_u32(&ctl.p_full[half]), cp & 1)) break;
+                                for (uint32_t piece = 0; piece < 2; ++piece) {
+                                    if (!need(smem_u32(&ctl.p_full[piece]), cp & 1)) break;
                                     tc_fence_after();
-                                    accumulate(tmem + T_A0, tmem + T_S, b, half, half == 0 && i == 1);
+                                    accumulate(tmem + T_A0, tmem + T_S, b, piece, piece == 0 && i == 1);
                                 }
                                 if (!ok) break;
                                 mma_commit(smem_u32(KV ? &ctl.b1_empty[sp] : &ctl.b0_empty[sp]));
                             }
                             if (i == nc) break;
+                            // S: the arithmetic has read the chunk before's (it may be another kind of item's)
+                            if ((!two || i == 0) && c > 0 && !need(smem_u32(&ctl.p_full[0]), cp & 1)) break;
                             tc_fence_after();
                             product(tmem + T_S, sbase + L::A0, sbase + L::B0 + st0 * L::TILE);
-                            mma_commit(smem_u32(&ctl.s_full));
+                            mma_commit(smem_u32(&ctl.s_full[c & 1]));
+                            if (!two) mma_commit(smem_u32(&ctl.b0_empty[st0]));
                             if (i == nc - 1) mma_commit(smem_u32(&ctl.a_empty));
                         }
                     } else {
@@ -690,24 +722,29 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                             const uint32_t cp = c - 1;
                             const uint32_t st1 = c % NS1, sp = cp % NS0;
                             if (i < nc && !need(smem_u32(&ctl.b1_full[st1]), (c / NS1) & 1)) break;
+                            // the accumulators, and without A0 the second dP buffer in its columns
+                            if (i == 1 && !need(smem_u32(&ctl.acc_free), (n_seq & 1) ^ 1)) break;
+                            auto dp = [&]() {
+                                tc_fence_after();
+                                product(tmem + (!two && (i & 1) ? T_A0 : T_DP), sbase + L::A1, sbase + L::B1 + st1 * L::TILE);
+                                mma_commit(smem_u32(&ctl.dp_full[c & 1]));
+                                if (!KV) mma_commit(smem_u32(&ctl.b1_empty[st1]));
+                                if (i == nc - 1) mma_commit(smem_u32(&ctl.a_empty));
+                            };
+                            if (!two && i < nc) dp();
                             if (i > 0) {
-                                if (i == 1 && !need(smem_u32(&ctl.acc_free), (n_seq & 1) ^ 1)) break;
                                 if (!need(smem_u32(&ctl.b0_full[sp]), (cp / NS0) & 1)) break;
-#pragma unroll
-                                for (uint32_t half = 0; half < 2; ++half) {
-                                    if (!need(smem_u32(&ctl.ds_full[half]), cp & 1)) break;
-                                    tc_fence_after();
-                                    accumulate(tmem + T_A1, tmem + T_DP, sbase + L::B0 + sp * L::TILE, half, half == 0 && i == 1);
-                                }
-                                if (!ok) break;
+                                if (!need(smem_u32(&ctl.ds_full[cp & 1]), (cp >> 1) & 1)) break;
+                                if (two && i < nc && !need(smem_u32(&ctl.s_full[c & 1]), (c >> 1) & 1)) break;
+                                tc_fence_after();
+                                const uint32_t ds = tmem + (!two && !(i & 1) ? T_A0 : T_DP);
+                                const uint32_t b = sbase + L::B0 + sp * L::TILE;
+                                accumulate(tmem + T_A1, ds, b, 0, i == 1);
+                                accumulate(tmem + T_A1, ds, b, 1, false);
                                 mma_commit(smem_u32(&ctl.b0_empty[sp]));
                             }
                             if (i == nc) break;
-                            tc_fence_after();
-                            product(tmem + T_DP, sbase + L::A1, sbase + L::B1 + st1 * L::TILE);
-                            mma_commit(smem_u32(&ctl.dp_full));
-                            if (!KV) mma_commit(smem_u32(&ctl.b1_empty[st1]));
-                            if (i == nc - 1) mma_commit(smem_u32(&ctl.a_empty));
+                            if (two) dp();
                         }
                     }
                     if (!ok) break;
@@ -732,16 +769,18 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
 
 // First `stat_blocks` CTAs: -lse * log2(e) and -dO . O of every row (one warp
 // per 8 rows; 16 bytes of O and dO a lane), the former -inf for padding rows
-// and rows that keep no block, so that their P is 0.  The others: one warp
+// and rows that keep no block, so that their P is 0; and for each 8 rows the
+// largest |O|^2 and the sum of |v|^2.  The others: one warp
 // per (b, h, query block) writes its kv list as a bit row.
 template <int D>
 __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, int nwords,
                                                         const uint4* __restrict__ o, const uint4* __restrict__ dout,
+                                                        const uint4* __restrict__ v,
                                                         const float* __restrict__ lse,
                                                         const int32_t* __restrict__ kv_idx,
                                                         const int32_t* __restrict__ kv_cnt,
                                                         float* __restrict__ nlse2, float* __restrict__ ndelta,
-                                                        uint32_t* __restrict__ bits) {
+                                                        float2* __restrict__ norms, uint32_t* __restrict__ bits) {
     extern __shared__ uint32_t gp_bits[];   // [8][nwords]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (static_cast<int>(blockIdx.x) < stat_blocks) {
@@ -750,26 +789,43 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, 
         const long long rows = static_cast<long long>(g.B) * g.H * g.Npad;
         const long long row0 = (static_cast<long long>(blockIdx.x) * 8 + warp) * 8;
         if (row0 >= rows) return;
-        uint4 x[8 / RPI], y[8 / RPI];        // Npad is a multiple of 16: the 8 rows exist
+        uint4 x[8 / RPI], y[8 / RPI], z[8 / RPI];   // Npad is a multiple of 16: the 8 rows exist
 #pragma unroll
         for (int i = 0; i < 8 / RPI; ++i) {
             const long long at = (row0 + i * RPI) * LPR + lane;
             x[i] = __ldg(o + at);
             y[i] = __ldg(dout + at);
+            z[i] = __ldg(v + at);
         }
+        float o2max = 0.f, v2 = 0.f;
 #pragma unroll
         for (int i = 0; i < 8 / RPI; ++i) {
             const uint32_t xa[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ya[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
-            float s = 0.f;
+            const uint32_t za[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
+            float s = 0.f, o2 = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                s = fmaf(__uint_as_float(xa[k] << 16), __uint_as_float(ya[k] << 16), s);
-                s = fmaf(__uint_as_float(xa[k] & 0xFFFF0000u), __uint_as_float(ya[k] & 0xFFFF0000u), s);
+                const float x0 = __uint_as_float(xa[k] << 16), x1 = __uint_as_float(xa[k] & 0xFFFF0000u);
+                const float z0 = __uint_as_float(za[k] << 16), z1 = __uint_as_float(za[k] & 0xFFFF0000u);
+                s = fmaf(x0, __uint_as_float(ya[k] << 16), s);
+                s = fmaf(x1, __uint_as_float(ya[k] & 0xFFFF0000u), s);
+                o2 = fmaf(x0, x0, fmaf(x1, x1, o2));
+                v2 = fmaf(z0, z0, fmaf(z1, z1, v2));
             }
 #pragma unroll
-            for (int d = LPR / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            for (int d = LPR / 2; d > 0; d >>= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, d);
+                o2 += __shfl_xor_sync(0xffffffffu, o2, d);
+            }
+            o2max = fmaxf(o2max, o2);
             if (lane % LPR == 0) ndelta[row0 + i * RPI + lane / LPR] = -s;
         }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            o2max = fmaxf(o2max, __shfl_xor_sync(0xffffffffu, o2max, d));
+            v2 += __shfl_xor_sync(0xffffffffu, v2, d);
+        }
+        if (lane == 0) norms[row0 / 8] = make_float2(o2max, v2);
         if (lane < 8) {
             const long long r = row0 + lane;
             int f_, y_, x_;
@@ -867,15 +923,33 @@ __global__ void __launch_bounds__(256) grad_lists_kernel(Geo g, int G, int ngrou
 
 // One CTA per (direction, b, h): the head's tiles by list length, longest
 // first (a counting sort; which of two equal tiles comes first changes only
-// the schedule).  The first CTA of a direction resets its item counter.
-__global__ void __launch_bounds__(256) grad_order_kernel(int BH, int ngroups, int nb, const int32_t* __restrict__ cntq,
+// the schedule), query tiles that need the exact delta with GRAD_FLAG.  The
+// first CTA of a direction resets its item counter.
+__global__ void __launch_bounds__(256) grad_order_kernel(Geo g, int G, int ngroups, const float2* __restrict__ norms,
+                                                         const int32_t* __restrict__ cntq,
                                                          const int32_t* __restrict__ cntk, int32_t* __restrict__ ordq,
                                                          int32_t* __restrict__ ordk, int* __restrict__ counters) {
+    const int BH = g.B * g.H, nb = g.nb;
+    __shared__ float part[256];
     extern __shared__ int go_start[];   // [nb + 1]
     const int dir = static_cast<int>(blockIdx.x) / BH, bh = static_cast<int>(blockIdx.x) - dir * BH;
     const int32_t* cnt = (dir ? cntk : cntq) + static_cast<long long>(bh) * ngroups;
     int32_t* ord = (dir ? ordk : ordq) + static_cast<long long>(bh) * ngroups;
     if (bh == 0 && threadIdx.x == 0) counters[dir] = 0;
+    const int n8 = static_cast<int>(g.Npad / 8);
+    norms += static_cast<long long>(bh) * n8;
+    float limit = 0.f;
+    if (dir == 0) {
+        float v2 = 0.f;
+        for (int i = threadIdx.x; i < n8; i += 256) v2 += norms[i].y;
+        part[threadIdx.x] = v2;
+        __syncthreads();
+        for (int d = 128; d > 0; d >>= 1) {
+            if (static_cast<int>(threadIdx.x) < d) part[threadIdx.x] += part[threadIdx.x + d];
+            __syncthreads();
+        }
+        limit = GRAD_EXACT * part[0] / static_cast<float>(g.N);
+    }
     for (int i = threadIdx.x; i <= nb; i += blockDim.x) go_start[i] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < ngroups; i += blockDim.x) atomicAdd(&go_start[nb - cnt[i]], 1);
@@ -896,7 +970,16 @@ __global__ void __launch_bounds__(256) grad_order_kernel(int BH, int ngroups, in
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < ngroups; i += blockDim.x) ord[atomicAdd(&go_start[nb - cnt[i]], 1)] = i;
+    for (int i = threadIdx.x; i < ngroups; i += blockDim.x) {
+        int entry = i;
+        if (dir == 0) {
+            const int at = i * G * g.bs / 8, n = min(G * g.bs / 8, n8 - at);
+            float o2 = 0.f;
+            for (int k = 0; k < n; ++k) o2 = fmaxf(o2, norms[at + k].x);
+            if (o2 > limit) entry |= GRAD_FLAG;
+        }
+        ord[atomicAdd(&go_start[nb - cnt[i]], 1)] = entry;
+    }
 }
 
 // Every block's real extent.
@@ -908,7 +991,7 @@ __global__ void __launch_bounds__(256) grad_extent_kernel(Geo g, int32_t* __rest
 // ------------------------------------------------------------------ host side
 
 struct GradWs {
-    size_t nlse2, ndelta, bits, ulq, ulk, cntq, cntk, ordq, ordk, ext, counters, total;
+    size_t nlse2, ndelta, norms, bits, ulq, ulk, cntq, cntk, ordq, ordk, ext, counters, total;
     int G, ngroups, nwords;
 };
 
@@ -922,7 +1005,8 @@ static GradWs grad_ws(const fvattn_geom& g) {
     const size_t units = BH * w.ngroups;
     w.nlse2 = 0;
     w.ndelta = w.nlse2 + al(4 * BH * g.Npad);
-    w.bits = w.ndelta + al(4 * BH * g.Npad);
+    w.norms = w.ndelta + al(4 * BH * g.Npad);
+    w.bits = w.norms + al(BH * g.Npad);
     w.ulq = w.bits + al(4 * BH * nb * w.nwords);
     w.ulk = w.ulq + al(4 * units * nb);
     w.cntq = w.ulk + al(4 * units * nb);
@@ -961,6 +1045,7 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
     const long long rows = static_cast<long long>(BH) * g.Npad;
     float* nlse2 = reinterpret_cast<float*>(ws + wl.nlse2);
     float* ndelta = reinterpret_cast<float*>(ws + wl.ndelta);
+    float2* norms = reinterpret_cast<float2*>(ws + wl.norms);
     uint32_t* bits = reinterpret_cast<uint32_t*>(ws + wl.bits);
     uint32_t* ulq = reinterpret_cast<uint32_t*>(ws + wl.ulq);
     uint32_t* ulk = reinterpret_cast<uint32_t*>(ws + wl.ulk);
@@ -985,16 +1070,16 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
     const int stat_blocks = static_cast<int>((rows + 63) / 64);
     const int bit_blocks = static_cast<int>((static_cast<long long>(BH) * g.nb + 7) / 8);
     grad_prep_kernel<D><<<stat_blocks + bit_blocks, 256, sizeof(uint32_t) * 8 * wl.nwords, s>>>(
-        g, stat_blocks, wl.nwords, static_cast<const uint4*>(o_t), static_cast<const uint4*>(do_t), lse, kv_idx, kv_cnt,
-        nlse2, ndelta, bits);
+        g, stat_blocks, wl.nwords, static_cast<const uint4*>(o_t), static_cast<const uint4*>(do_t),
+        static_cast<const uint4*>(v_t), lse, kv_idx, kv_cnt, nlse2, ndelta, norms, bits);
     FV_CHECK_LAUNCH();
     grad_extent_kernel<<<(g.nb + 255) / 256, 256, 0, s>>>(g, ext);
     FV_CHECK_LAUNCH();
     grad_lists_kernel<<<static_cast<unsigned>((2ll * BH * wl.ngroups + 7) / 8), 256, 0, s>>>(
         g, wl.G, wl.ngroups, wl.nwords, bits, ulq, cntq, ulk, cntk);
     FV_CHECK_LAUNCH();
-    grad_order_kernel<<<2 * BH, 256, sizeof(int) * (g.nb + 1), s>>>(BH, wl.ngroups, g.nb, cntq, cntk, ordq, ordk,
-                                                                    counters);
+    grad_order_kernel<<<2 * BH, 256, sizeof(int) * (g.nb + 1), s>>>(g, wl.G, wl.ngroups, norms, cntq, cntk, ordq,
+                                                                    ordk, counters);
     FV_CHECK_LAUNCH();
 
     GradArgs a;
