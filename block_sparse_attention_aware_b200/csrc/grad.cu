@@ -67,6 +67,7 @@ constexpr int GRAD_THREADS = 384;
 // over one and a half chunks' time: a stage more.
 constexpr int GRAD_STAGES0 = 3, GRAD_STAGES1 = 2;
 constexpr uint32_t GRAD_TMEM = 512;
+constexpr uint32_t GRAD_POLY = 0x00;     // which of 8 pairs of columns take their exponentials on the FMA pipe
 constexpr float GRAD_EXACT = 1.f / 16.f;
 constexpr int GRAD_FLAG = 1 << 30;   // in the work order: a query tile that needs the exact delta
 constexpr int GRAD_GROUP = 8;     // blocks per tile at bs = 16
@@ -135,6 +136,29 @@ __device__ __forceinline__ int grad_extent(const Geo& g, int block) {
     const int by = rest % g.nby;
     const int bf = rest / g.nby;
     return min(g.tf, g.F - bf * g.tf) | (min(g.th, g.Hs - by * g.th) << 8) | (min(g.tw, g.Ws - bx * g.tw) << 16);
+}
+
+// 2^x for two values on the FMA pipe: x = n + f with n the nearest integer
+// (the low bits of x + 1.5 * 2^23), 2^f by a polynomial of degree 4 fitted to
+// the relative error on [-1/2, 1/2] (2^-18.5), n added to the exponent.  x is
+// taken as at least -125, and at most 127 by the caller; NaN gives a result
+// that is not finite after rounding to bf16.
+__device__ __forceinline__ void exp2_poly(float& x0, float& x1) {
+    asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x0));
+    asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x1));
+    const unsigned long long x = f2_pack(x0, x1);
+    const unsigned long long magic = f2_pack(12582912.f, 12582912.f), neg = f2_pack(-12582912.f, -12582912.f);
+    const unsigned long long t = f2_add(x, magic);
+    const unsigned long long f = f2_fma(f2_add(t, neg), f2_pack(-1.f, -1.f), x);
+    unsigned long long p = f2_fma(f2_pack(9.570101276e-3f, 9.570101276e-3f), f, f2_pack(5.591785908e-2f, 5.591785908e-2f));
+    p = f2_fma(p, f, f2_pack(2.402474433e-1f, 2.402474433e-1f));
+    p = f2_fma(p, f, f2_pack(6.931217909e-1f, 6.931217909e-1f));
+    p = f2_fma(p, f, f2_pack(9.999992847e-1f, 9.999992847e-1f));
+    float t0, t1, p0, p1;
+    f2_unpack(t, t0, t1);
+    f2_unpack(p, p0, p1);
+    x0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+    x1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
 }
 
 // One slot of a chunk: its block (-1: none) and membership bits.
@@ -326,8 +350,12 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                                     float x0, x1;
                                     f2_unpack(f2_fma(f2_pack(__uint_as_float(pv[h][e + z]), __uint_as_float(pv[h][e + z + 1])),
                                                      sl2x2, z ? add.y : add.x), x0, x1);
-                                    x0 = ex2_approx(x0);
-                                    x1 = ex2_approx(x1);
+                                    if ((GRAD_POLY >> (((e + z) >> 1) & 7)) & 1) {
+                                        exp2_poly(x0, x1);
+                                    } else {
+                                        x0 = ex2_approx(x0);
+                                        x1 = ex2_approx(x1);
+                                    }
                                     if (!FULL) {
                                         x0 = (mw[h] & (1u << (e + z))) ? x0 : 0.f;
                                         x1 = (mw[h] & (1u << (e + z + 1))) ? x1 : 0.f;
