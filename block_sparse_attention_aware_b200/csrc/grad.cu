@@ -34,8 +34,8 @@
 //               each chunk's masks
 //   warp 2      producer of the other streamed tensor (KV: dO; else V)
 //   warps 1, 3  one lane each issues MMAs
-//   warps 4..11 two groups of four warps; a thread has one row of the
-//               128-row tile and half of the chunk's 128 columns: P and dS
+//   warps 4..19 four groups of four warps; a thread has one row of the
+//               128-row tile and a quarter of the chunk's 128 columns: P and dS
 //               are formed from the fp32 S and dP in tensor memory and go
 //               back there as bf16, where they are the A operand of the
 //               accumulating products
@@ -62,19 +62,20 @@
 
 namespace fv {
 
-constexpr int GRAD_THREADS = 384;
+constexpr int GRAD_GROUPS = 4;    // warpgroups of arithmetic, 32 columns of a chunk each
+constexpr int GRAD_WARPS = 4 * GRAD_GROUPS;
+constexpr int GRAD_THREADS = 128 * (1 + GRAD_GROUPS);
 // The first streamed tensor is held from S to the last product of its chunk,
 // over one and a half chunks' time: a stage more.
 constexpr int GRAD_STAGES0 = 3, GRAD_STAGES1 = 2;
 constexpr uint32_t GRAD_TMEM = 512;
-constexpr uint32_t GRAD_POLY = 0x00;     // which of 8 pairs of columns take their exponentials on the FMA pipe
 constexpr float GRAD_EXACT = 1.f / 16.f;
 constexpr int GRAD_FLAG = 1 << 30;   // in the work order: a query tile that needs the exact delta
 constexpr int GRAD_GROUP = 8;     // blocks per tile at bs = 16
-// Register split (setmaxnreg): the launch gives 168 a thread; one warpgroup
-// of producers and issuer at LOW, two of arithmetic at HIGH.
-constexpr int GRAD_LAUNCH_REGS = 168, GRAD_LOW = 72, GRAD_HIGH = 216;
-static_assert(128 * GRAD_LOW + 256 * GRAD_HIGH <= GRAD_THREADS * GRAD_LAUNCH_REGS, "register split");
+// Register split (setmaxnreg): the launch gives 96 a thread; one warpgroup
+// of producers and issuers at LOW, the arithmetic at HIGH.
+constexpr int GRAD_LAUNCH_REGS = 96, GRAD_LOW = 64, GRAD_HIGH = 104;
+static_assert(128 * (GRAD_LOW + GRAD_GROUPS * GRAD_HIGH) <= GRAD_THREADS * GRAD_LAUNCH_REGS, "register split");
 
 // Tensor-memory columns: S (P over it), dP (dS over it), the two accumulators.
 constexpr uint32_t T_S = 0, T_DP = 128, T_A0 = 256, T_A1 = 384;
@@ -99,7 +100,7 @@ struct GradArgs {
 
 struct __align__(16) GradCtrl {
     // KV: the chunks' column statistics, -lse2 of the first ring's stages and then -delta of the second's.
-    // Else: sums of P dP by row, [item's parity][team]
+    // Else: each column group's sum of P dP by row
     float stat[GRAD_STAGES0 + GRAD_STAGES1][128];
     uint32_t mask[GRAD_STAGES0][8];                              // 4 words of columns that are tokens, then a
                                                                  // byte a slot: blocks of the tile paired with it
@@ -138,29 +139,6 @@ __device__ __forceinline__ int grad_extent(const Geo& g, int block) {
     return min(g.tf, g.F - bf * g.tf) | (min(g.th, g.Hs - by * g.th) << 8) | (min(g.tw, g.Ws - bx * g.tw) << 16);
 }
 
-// 2^x for two values on the FMA pipe: x = n + f with n the nearest integer
-// (the low bits of x + 1.5 * 2^23), 2^f by a polynomial of degree 4 fitted to
-// the relative error on [-1/2, 1/2] (2^-18.5), n added to the exponent.  x is
-// taken as at least -125, and at most 127 by the caller; NaN gives a result
-// that is not finite after rounding to bf16.
-__device__ __forceinline__ void exp2_poly(float& x0, float& x1) {
-    asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x0));
-    asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x1));
-    const unsigned long long x = f2_pack(x0, x1);
-    const unsigned long long magic = f2_pack(12582912.f, 12582912.f), neg = f2_pack(-12582912.f, -12582912.f);
-    const unsigned long long t = f2_add(x, magic);
-    const unsigned long long f = f2_fma(f2_add(t, neg), f2_pack(-1.f, -1.f), x);
-    unsigned long long p = f2_fma(f2_pack(9.570101276e-3f, 9.570101276e-3f), f, f2_pack(5.591785908e-2f, 5.591785908e-2f));
-    p = f2_fma(p, f, f2_pack(2.402474433e-1f, 2.402474433e-1f));
-    p = f2_fma(p, f, f2_pack(6.931217909e-1f, 6.931217909e-1f));
-    p = f2_fma(p, f, f2_pack(9.999992847e-1f, 9.999992847e-1f));
-    float t0, t1, p0, p1;
-    f2_unpack(t, t0, t1);
-    f2_unpack(p, p0, p1);
-    x0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-    x1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-}
-
 // One slot of a chunk: its block (-1: none) and membership bits.
 __device__ __forceinline__ int grad_slot(const uint32_t* ul, int e, int cnt, uint32_t& mem) {
     mem = 0u;
@@ -170,21 +148,17 @@ __device__ __forceinline__ int grad_slot(const uint32_t* ul, int e, int cnt, uin
     return static_cast<int>(v & 0xFFFFFFu);
 }
 
-// Columns 64 w .. of a chunk that a row of the tile's block tb sees, 32 a
-// word: those of slots whose block is paired with tb, and tokens (unless
-// `all`).  lbs = log2(bs).
-__device__ __forceinline__ void grad_mask(const uint32_t* m, int lbs, int tb, int w, bool all, uint32_t (&mw)[2]) {
-    const uint2 pad = *reinterpret_cast<const uint2*>(m + 2 * w);
+// Columns 32 w .. of a chunk that a row of the tile's block tb sees: those of
+// slots whose block is paired with tb, and tokens (unless `all`).  lbs =
+// log2(bs).
+__device__ __forceinline__ uint32_t grad_mask(const uint32_t* m, int lbs, int tb, int w, bool all) {
+    const uint32_t pad = m[w];
     const uint2 by = *reinterpret_cast<const uint2*>(m + 4);
     const unsigned long long mem = ((static_cast<unsigned long long>(by.y) << 32) | by.x) >> tb;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int col = w * 64 + q * 32;
-        const uint32_t lo = static_cast<uint32_t>(mem >> (8 * (col >> lbs))) & 1u;
-        const uint32_t hi = static_cast<uint32_t>(mem >> (8 * ((col + 16) >> lbs))) & 1u;   // another slot at bs = 16
-        mw[q] = (lo ? 0x0000FFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
-        if (!all) mw[q] &= q ? pad.y : pad.x;
-    }
+    const uint32_t lo = static_cast<uint32_t>(mem >> (8 * ((w * 32) >> lbs))) & 1u;
+    const uint32_t hi = static_cast<uint32_t>(mem >> (8 * ((w * 32 + 16) >> lbs))) & 1u;   // another slot at bs = 16
+    const uint32_t mw = (lo ? 0x0000FFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+    return all ? mw : mw & pad;
 }
 
 template <int D, bool KV>
@@ -218,23 +192,23 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
         mbar_init(smem_u32(&ctl.a_empty), 2);
         for (int s = 0; s < NS0; ++s) {
             mbar_init(smem_u32(&ctl.b0_full[s]), 1);
-            mbar_init(smem_u32(&ctl.b0_empty[s]), (KV ? 1 : 2) + 8);   // commits of its last products, the arithmetic warps
+            mbar_init(smem_u32(&ctl.b0_empty[s]), (KV ? 1 : 2) + GRAD_WARPS);   // commits of its last products, the arithmetic
         }
         for (int s = 0; s < NS1; ++s) {
             mbar_init(smem_u32(&ctl.b1_full[s]), 1);
-            mbar_init(smem_u32(&ctl.b1_empty[s]), KV ? 1 + 8 : 1);
+            mbar_init(smem_u32(&ctl.b1_empty[s]), KV ? 1 + GRAD_WARPS : 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&ctl.s_full[s]), 1);
             mbar_init(smem_u32(&ctl.dp_full[s]), 1);
-            mbar_init(smem_u32(&ctl.p_full[s]), 8);
-            mbar_init(smem_u32(&ctl.ds_full[s]), 8);
+            mbar_init(smem_u32(&ctl.p_full[s]), GRAD_WARPS);
+            mbar_init(smem_u32(&ctl.ds_full[s]), GRAD_WARPS);
             mbar_init(smem_u32(&ctl.item_full[s]), 1);
-            mbar_init(smem_u32(&ctl.item_empty[s]), 2 + 1 + 8);   // issuers, second producer, arithmetic
+            mbar_init(smem_u32(&ctl.item_empty[s]), 2 + 1 + GRAD_WARPS);   // issuers, second producer, arithmetic
         }
-        mbar_init(smem_u32(&ctl.sum_full), 8);
+        mbar_init(smem_u32(&ctl.sum_full), GRAD_WARPS);
         mbar_init(smem_u32(&ctl.acc_full), 2);
-        mbar_init(smem_u32(&ctl.acc_free), 8);
+        mbar_init(smem_u32(&ctl.acc_free), GRAD_WARPS);
         for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&ctl.drain[s]), 1);
         ctl.abort_flag = 0;
         fence_mbar_init();
@@ -257,11 +231,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
     if (warp >= 4) {
         regs_inc<GRAD_HIGH>();
         // =========================== arithmetic: P, dS, epilogue
-        const int w = (warp - 4) >> 2;              // columns 64 w ..
+        const int w = (warp - 4) >> 2;              // columns 32 w ..
         const int quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        const uint32_t sbuf = trow + T_S + static_cast<uint32_t>(w) * 64u;
+        const uint32_t sbuf = trow + T_S + static_cast<uint32_t>(w) * 32u;
         const int tb = row / bs;                    // this row's block in the tile
         const unsigned long long sl2x2 = f2_pack(a.scale_log2, a.scale_log2);
         int item_seq = 0;
@@ -304,19 +278,17 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
             }
             for (int i = 0; i < nc; ++i, ++c) {
                 const uint32_t st0 = c % NS0, st1 = c % NS1, par = c & 1, ph = (c >> 1) & 1;
-                const uint32_t dpbuf = trow + (!two && (i & 1) ? T_A0 : T_DP) + static_cast<uint32_t>(w) * 64u;
+                const uint32_t dpbuf = trow + (!two && (i & 1) ? T_A0 : T_DP) + static_cast<uint32_t>(w) * 32u;
                 if (!wait_warp2(smem_u32(&ctl.b0_full[st0]), (c / NS0) & 1, smem_u32(&ctl.s_full[par]), ph, abort_flag,
                                 wlim)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t pv[2][32];                 // S, then P, of this row: 32 columns each
-                tmem_ld32(sbuf, pv[0]);
-                tmem_ld32(sbuf + 32u, pv[1]);
-                uint32_t mw[2];                     // columns that the row sees
-                grad_mask(ctl.mask[st0], lbs, tb, w, all, mw);
-                const bool full = __all_sync(0xffffffffu, (mw[0] & mw[1]) == 0xFFFFFFFFu);
+                uint32_t pv[32];                    // S, then P, of this row
+                tmem_ld32(sbuf, pv);
+                uint32_t mw = grad_mask(ctl.mask[st0], lbs, tb, w, all);   // columns that the row sees
+                const bool full = __all_sync(0xffffffffu, mw == 0xFFFFFFFFu);
                 tmem_wait_ld();
                 // The whole chunk's arithmetic is there twice: without masks, and with a select an element.
                 // One body that tests for masks on the way took twice the time, masks or not.
@@ -336,38 +308,32 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                             mbar_arrive(smem_u32(&ctl.b0_empty[st0]));
                         }
                     }
+                    const ulonglong2* nls = reinterpret_cast<const ulonglong2*>(&ctl.stat[st0][w * 32]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {   // P over S, for half of its product
-                        uint32_t pk[16];
-                        {
-                            const ulonglong2* nls = reinterpret_cast<const ulonglong2*>(&ctl.stat[st0][w * 64 + h * 32]);
+                        uint32_t pk[8];
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                ulonglong2 add = make_ulonglong2(nl2, nl2);
-                                if (KV) add = nls[e >> 2];
+                        for (int e = h * 16; e < h * 16 + 16; e += 4) {
+                            ulonglong2 add = make_ulonglong2(nl2, nl2);
+                            if (KV) add = nls[e >> 2];
 #pragma unroll
-                                for (int z = 0; z < 4; z += 2) {
-                                    float x0, x1;
-                                    f2_unpack(f2_fma(f2_pack(__uint_as_float(pv[h][e + z]), __uint_as_float(pv[h][e + z + 1])),
-                                                     sl2x2, z ? add.y : add.x), x0, x1);
-                                    if ((GRAD_POLY >> (((e + z) >> 1) & 7)) & 1) {
-                                        exp2_poly(x0, x1);
-                                    } else {
-                                        x0 = ex2_approx(x0);
-                                        x1 = ex2_approx(x1);
-                                    }
-                                    if (!FULL) {
-                                        x0 = (mw[h] & (1u << (e + z))) ? x0 : 0.f;
-                                        x1 = (mw[h] & (1u << (e + z + 1))) ? x1 : 0.f;
-                                    }
-                                    pv[h][e + z] = __float_as_uint(x0);
-                                    pv[h][e + z + 1] = __float_as_uint(x1);
-                                    if (TWO) pk[(e + z) >> 1] = pack_bf16x2(x0, x1);
+                            for (int z = 0; z < 4; z += 2) {
+                                float x0, x1;
+                                f2_unpack(f2_fma(f2_pack(__uint_as_float(pv[e + z]), __uint_as_float(pv[e + z + 1])), sl2x2,
+                                                 z ? add.y : add.x), x0, x1);
+                                x0 = ex2_approx(x0);
+                                x1 = ex2_approx(x1);
+                                if (!FULL) {
+                                    x0 = (mw & (1u << (e + z))) ? x0 : 0.f;
+                                    x1 = (mw & (1u << (e + z + 1))) ? x1 : 0.f;
                                 }
+                                pv[e + z] = __float_as_uint(x0);
+                                pv[e + z + 1] = __float_as_uint(x1);
+                                if (TWO) pk[((e + z) >> 1) & 7] = pack_bf16x2(x0, x1);
                             }
                         }
                         if constexpr (TWO) {
-                            tmem_st16(sbuf + h * 16u, pk);
+                            tmem_st8(sbuf + h * 8u, pk);
                             tmem_wait_st();
                             tc_fence_before();
                             __syncwarp();
@@ -385,43 +351,35 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                         return false;
                     }
                     tc_fence_after();
-                    uint32_t dv[2][32];
-                    tmem_ld32(dpbuf, dv[0]);
-                    tmem_ld32(dpbuf + 32u, dv[1]);
+                    uint32_t dv[32], ds[16];
+                    tmem_ld32(dpbuf, dv);
                     tmem_wait_ld();
+                    // (the bits' tests are made again: kept from above they would take 32 registers)
+                    if (!FULL) asm volatile("" : "+r"(mw));
+                    const ulonglong2* nds = reinterpret_cast<const ulonglong2*>(&ctl.stat[NS0 + st1][w * 32]);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t ds[16];
-                        {
-                            // (the bits' tests are made again: kept from above they would take 64 registers)
-                            if (!FULL) asm volatile("" : "+r"(mw[h]));
-                            const ulonglong2* nds = reinterpret_cast<const ulonglong2*>(&ctl.stat[NS0 + st1][w * 64 + h * 32]);
+                    for (int e = 0; e < 32; e += 4) {
+                        ulonglong2 add = make_ulonglong2(nd2, nd2);
+                        if (KV) add = nds[e >> 2];
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                ulonglong2 add = make_ulonglong2(nd2, nd2);
-                                if (KV) add = nds[e >> 2];
-#pragma unroll
-                                for (int z = 0; z < 4; z += 2) {
-                                    float x0 = __uint_as_float(dv[h][e + z]), x1 = __uint_as_float(dv[h][e + z + 1]);
-                                    if (!FULL && !KV) {   // nothing of a masked pair enters the sum
-                                        x0 = (mw[h] & (1u << (e + z))) ? x0 : 0.f;
-                                        x1 = (mw[h] & (1u << (e + z + 1))) ? x1 : 0.f;
-                                    }
-                                    const unsigned long long dp2 = f2_pack(x0, x1);
-                                    const unsigned long long p2 =
-                                        f2_pack(__uint_as_float(pv[h][e + z]), __uint_as_float(pv[h][e + z + 1]));
-                                    if (!KV) sum2 = f2_fma(p2, dp2, sum2);
-                                    f2_unpack(f2_mul(f2_add(dp2, z ? add.y : add.x), p2), x0, x1);
-                                    if (!FULL && KV) {    // 0 whatever dP and the column's statistics hold
-                                        x0 = (mw[h] & (1u << (e + z))) ? x0 : 0.f;
-                                        x1 = (mw[h] & (1u << (e + z + 1))) ? x1 : 0.f;
-                                    }
-                                    ds[(e + z) >> 1] = pack_bf16x2(x0, x1);
-                                }
+                        for (int z = 0; z < 4; z += 2) {
+                            float x0 = __uint_as_float(dv[e + z]), x1 = __uint_as_float(dv[e + z + 1]);
+                            if (!FULL && !KV) {   // nothing of a masked pair enters the sum
+                                x0 = (mw & (1u << (e + z))) ? x0 : 0.f;
+                                x1 = (mw & (1u << (e + z + 1))) ? x1 : 0.f;
                             }
+                            const unsigned long long dp2 = f2_pack(x0, x1);
+                            const unsigned long long p2 = f2_pack(__uint_as_float(pv[e + z]), __uint_as_float(pv[e + z + 1]));
+                            if (!KV) sum2 = f2_fma(p2, dp2, sum2);
+                            f2_unpack(f2_mul(f2_add(dp2, z ? add.y : add.x), p2), x0, x1);
+                            if (!FULL && KV) {    // 0 whatever dP and the column's statistics hold
+                                x0 = (mw & (1u << (e + z))) ? x0 : 0.f;
+                                x1 = (mw & (1u << (e + z + 1))) ? x1 : 0.f;
+                            }
+                            ds[(e + z) >> 1] = pack_bf16x2(x0, x1);
                         }
-                        tmem_st16(dpbuf + h * 16u, ds);   // (all of dP has been read)
                     }
+                    tmem_st16(dpbuf, ds);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -438,51 +396,54 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 if (!ok) break;
             }
             if (!ok) break;
-            // ---- epilogue.  KV: columns' half 0 writes dV, 1 dK; else each writes half of dQ's columns.
+            // ---- epilogue.  KV: groups 0 and 1 write a half of dV each, 2 and 3 of dK; else each a quarter of dQ.
             float fix = 0.f;     // delta0 - delta
             if (nc > 0) {
                 if (!KV) {
                     float s0, s1;
                     f2_unpack(sum2, s0, s1);
-                    float* sums = ctl.stat[(n_seq & 1) * 2];   // the item before may still be read
-                    sums[w * 128 + row] = s0 + s1;
+                    // the sums of the item before have been read
+                    if (n_seq > 0 && !wait_warp(smem_u32(&ctl.acc_free), (n_seq - 1) & 1, abort_flag, wlim)) break;
+                    ctl.stat[w][row] = s0 + s1;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&ctl.sum_full));
                     if (!wait_warp(smem_u32(&ctl.sum_full), n_seq & 1, abort_flag, wlim)) break;
-                    const float nd1 = -(sums[row] + sums[128 + row]);
+                    const float nd1 = -((ctl.stat[0][row] + ctl.stat[1][row]) + (ctl.stat[2][row] + ctl.stat[3][row]));
                     fix = nd1 - nd;
                     if (live && w == 0) a.ndelta[grow] = nd1;
                 }
                 if (!wait_warp(smem_u32(&ctl.acc_full), n_seq & 1, abort_flag, wlim)) break;
                 tc_fence_after();
             }
-            const float f = KV && w == 0 ? 1.f : a.scale;
-            __nv_bfloat16* dst = (KV && w == 1 ? a.out1 : a.out0) + grow * D;
-            const uint32_t acc = trow + (KV && w == 0 ? T_A0 : T_A1);
-            constexpr int NQ = KV ? D / 32 : D / 64;
+            const bool first_out = KV && w < 2;
+            const float f = first_out ? 1.f : a.scale;
+            __nv_bfloat16* dst = (KV && !first_out ? a.out1 : a.out0) + grow * D;
+            const uint32_t acc = trow + (first_out ? T_A0 : T_A1);
+            constexpr int COLS = KV ? D / 2 : D / 4;       // of a thread
+            constexpr int STEP = COLS < 32 ? COLS : 32;
 #pragma unroll 1
-            for (int q = 0; q < NQ; ++q) {
-                const uint32_t col = (KV ? 0u : static_cast<uint32_t>(w) * (D / 2)) + q * 32u;
-                uint32_t r[32];
+            for (int q = 0; q < COLS / STEP; ++q) {
+                const uint32_t col = static_cast<uint32_t>(KV ? w & 1 : w) * COLS + q * STEP;
+                uint32_t r[STEP];
                 if (nc > 0) {   // (rows that take no part may hold anything: they get zero)
-                    tmem_ld32(acc + col, r);
+                    tmem_ld(acc + col, r);
                     if (!KV && two) {
-                        uint32_t pk[32];
-                        tmem_ld32(trow + T_A0 + col, pk);
+                        uint32_t pk[STEP];
+                        tmem_ld(trow + T_A0 + col, pk);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < STEP; ++e)
                             r[e] = __float_as_uint(fmaf(fix, __uint_as_float(pk[e]), __uint_as_float(r[e])));
                     } else {
                         tmem_wait_ld();
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = 0u;
+                    for (int e = 0; e < STEP; ++e) r[e] = 0u;
                 }
                 if (in_tile) {
 #pragma unroll
-                    for (int v8 = 0; v8 < 4; ++v8) {
+                    for (int v8 = 0; v8 < STEP / 8; ++v8) {
                         uint32_t o[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -686,17 +647,15 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                         mma_bf16_ss(d, desc_of(abase + off, HI), desc_of(bbase + off, HI), ID_SS, kk > 0 ? 1u : 0u);
                     }
                 };
-                // acc += A (bf16 in tensor memory, 64 columns of K in each of two 64-column halves) x chunk
-                // (B, its 128 rows are K): the steps of one 32-column piece of each half
+                // acc += A (bf16 in tensor memory, the 32 columns of K of group z in 16 at 32 z) x chunk (B, its
+                // 128 rows are K): the steps of one 16-column piece of each group
                 auto accumulate = [&](uint32_t d, uint32_t abuf, uint32_t bbase, uint32_t piece, bool first) {
                     bbase = (bbase >> 4) | ((16384u >> 4) << 16);
                     asm volatile("" : "+r"(bbase));
 #pragma unroll
-                    for (uint32_t z = 0; z < 4; ++z) {
-                        const uint32_t in = piece * 2u + (z & 1u), half = z >> 1;   // step of the half
-                        mma_bf16_ts(d, abuf + half * 64u + in * 8u, desc_of(bbase + (((half * 4u + in) * 2048u) >> 4), HI),
+                    for (uint32_t z = 0; z < 4; ++z)
+                        mma_bf16_ts(d, abuf + z * 32u + piece * 8u, desc_of(bbase + (((z * 2u + piece) * 2048u) >> 4), HI),
                                     ID_ACC, (z > 0 || !first) ? 1u : 0u);
-                    }
                 };
                 bool ok = true;
                 auto need = [&](uint32_t bar, uint32_t parity) {
@@ -1057,7 +1016,7 @@ static int launch_grad(const CUtensorMap& a0, const CUtensorMap& a1, const CUten
     // setmaxnreg waits for ever for registers that the CTA was not launched with
     cudaFuncAttributes fa;
     if (cudaFuncGetAttributes(&fa, grad_kernel<D, KV>) != cudaSuccess) return FVATTN_ERR_CUDA;
-    if (static_cast<long long>(fa.numRegs) * GRAD_THREADS < 128ll * GRAD_LOW + 256ll * GRAD_HIGH)
+    if (static_cast<long long>(fa.numRegs) * GRAD_THREADS < 128ll * (GRAD_LOW + GRAD_GROUPS * GRAD_HIGH))
         return FVATTN_ERR_UNSUPPORTED;
     grad_kernel<D, KV><<<grid, GRAD_THREADS, L::ALLOC, s>>>(a0, a1, b0, b1, args);
     FV_CHECK_LAUNCH();
