@@ -624,53 +624,64 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
             }
             __syncwarp();
         } else {
-            // =========================== MMA issuers (one lane each of warps 1 and 3)
+            // =========================== MMA issuers (warps 1 and 3)
             // Warp 1: A0 += P(i-1) B, S(i).  Warp 3: A1 += dS(i-1) B0, dP(i).  In each the second product
             // overwrites columns that the first reads: one thread's MMAs keep their order.  While one
             // thread waits on its barriers the other's MMAs run; with a single issuer the pipe ran dry at
             // every wait (4200 clocks a chunk where its four products take 2048).  The exponentials wait for
             // A0 and S only, so warp 3 holds its products back until S(i) is done: 3400 to 3000 clocks.
-            if (lane == 0) {
+            // The whole warp walks the loop, so that addresses and descriptors are warp-uniform values.
+            {
                 constexpr uint32_t ID_SS = idesc_bf16_f32(128, 128, false);
                 constexpr uint32_t ID_ACC = idesc_bf16_f32(128, D, true);
                 // A descriptor's upper half is one constant for all operands and the lower half holds the
                 // address: one add an operand.
                 constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
                 // C = own tile (A, K-major) x streamed chunk (B, K-major)
                 auto product = [&](uint32_t d, uint32_t abase, uint32_t bbase) {
                     abase = (abase >> 4) | (1u << 16);
                     bbase = (bbase >> 4) | (1u << 16);
-                    asm volatile("" : "+r"(abase), "+r"(bbase));   // (not kept for every step: they would spill)
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk >> 2) * 16384u + (kk & 3) * 32u) >> 4;
-                        mma_bf16_ss(d, desc_of(abase + off, HI), desc_of(bbase + off, HI), ID_SS, kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * 16384u + (kk & 3) * 32u) >> 4;
+                            mma_bf16_ss(d, desc_of(abase + off, HI), desc_of(bbase + off, HI), ID_SS, kk > 0 ? 1u : 0u);
+                        }
                     }
+                    __syncwarp();
                 };
                 // acc += A (bf16 in tensor memory, the 32 columns of K of group z in 16 at 32 z) x chunk (B, its
                 // 128 rows are K): the steps of one 16-column piece of each group
                 auto accumulate = [&](uint32_t d, uint32_t abuf, uint32_t bbase, uint32_t piece, bool first) {
                     bbase = (bbase >> 4) | ((16384u >> 4) << 16);
-                    asm volatile("" : "+r"(bbase));
+                    if (elect_one()) {
 #pragma unroll
-                    for (uint32_t z = 0; z < 4; ++z)
-                        mma_bf16_ts(d, abuf + z * 32u + piece * 8u, desc_of(bbase + (((z * 2u + piece) * 2048u) >> 4), HI),
-                                    ID_ACC, (z > 0 || !first) ? 1u : 0u);
+                        for (uint32_t z = 0; z < 4; ++z)
+                            mma_bf16_ts(d, abuf + z * 32u + piece * 8u,
+                                        desc_of(bbase + (((z * 2u + piece) * 2048u) >> 4), HI), ID_ACC,
+                                        (z > 0 || !first) ? 1u : 0u);
+                    }
+                    __syncwarp();
+                };
+                auto commit = [&](unsigned long long* bar) {
+                    if (elect_one()) mma_commit(smem_u32(bar));
+                    __syncwarp();
                 };
                 bool ok = true;
                 auto need = [&](uint32_t bar, uint32_t parity) {
-                    if (ok) ok = wait_bar(bar, parity, abort_flag, wlim);
+                    if (ok) ok = wait_warp(bar, parity, abort_flag, wlim);
                     return ok;
                 };
                 int item_seq = 0;
                 uint32_t n_seq = 0, c = 0;
-                const bool first_role = warp == 1;
+                const bool first_role = __shfl_sync(0xffffffffu, warp, 0) == 1;
                 while (ok) {
                     const int slot = item_seq & 1;
                     if (!need(smem_u32(&ctl.item_full[slot]), (item_seq >> 1) & 1)) break;
-                    const int kind = ctl.item[slot][3];
-                    const int cnt = ctl.item[slot][2];
-                    mbar_arrive(smem_u32(&ctl.item_empty[slot]));
+                    const int kind = __shfl_sync(0xffffffffu, ctl.item[slot][3], 0);
+                    const int cnt = __shfl_sync(0xffffffffu, ctl.item[slot][2], 0);
+                    if (lane == 0) mbar_arrive(smem_u32(&ctl.item_empty[slot]));
                     if (!kind) break;
                     const bool two = KV || kind == 2;
                     ++item_seq;
@@ -690,19 +701,19 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                                 for (uint32_t piece = 0; piece < 2; ++piece) {
                                     if (!need(smem_u32(&ctl.p_full[piece]), cp & 1)) break;
                                     tc_fence_after();
-                                    accumulate(tmem + T_A0, tmem + T_S, b, piece, piece == 0 && i == 1);
+                                    accumulate(tm + T_A0, tm + T_S, b, piece, piece == 0 && i == 1);
                                 }
                                 if (!ok) break;
-                                mma_commit(smem_u32(KV ? &ctl.b1_empty[sp] : &ctl.b0_empty[sp]));
+                                commit(KV ? &ctl.b1_empty[sp] : &ctl.b0_empty[sp]);
                             }
                             if (i == nc) break;
                             // S: the arithmetic has read the chunk before's (it may be another kind of item's)
                             if ((!two || i == 0) && c > 0 && !need(smem_u32(&ctl.p_full[0]), cp & 1)) break;
                             tc_fence_after();
-                            product(tmem + T_S, sbase + L::A0, sbase + L::B0 + st0 * L::TILE);
-                            mma_commit(smem_u32(&ctl.s_full[c & 1]));
-                            if (!two) mma_commit(smem_u32(&ctl.b0_empty[st0]));
-                            if (i == nc - 1) mma_commit(smem_u32(&ctl.a_empty));
+                            product(tm + T_S, sbase + L::A0, sbase + L::B0 + st0 * L::TILE);
+                            commit(&ctl.s_full[c & 1]);
+                            if (!two) commit(&ctl.b0_empty[st0]);
+                            if (i == nc - 1) commit(&ctl.a_empty);
                         }
                     } else {
                         for (int i = 0; i <= nc; ++i, ++c) {
@@ -713,10 +724,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                             if (i == 1 && !need(smem_u32(&ctl.acc_free), (n_seq & 1) ^ 1)) break;
                             auto dp = [&]() {
                                 tc_fence_after();
-                                product(tmem + (!two && (i & 1) ? T_A0 : T_DP), sbase + L::A1, sbase + L::B1 + st1 * L::TILE);
-                                mma_commit(smem_u32(&ctl.dp_full[c & 1]));
-                                if (!KV) mma_commit(smem_u32(&ctl.b1_empty[st1]));
-                                if (i == nc - 1) mma_commit(smem_u32(&ctl.a_empty));
+                                product(tm + (!two && (i & 1) ? T_A0 : T_DP), sbase + L::A1, sbase + L::B1 + st1 * L::TILE);
+                                commit(&ctl.dp_full[c & 1]);
+                                if (!KV) commit(&ctl.b1_empty[st1]);
+                                if (i == nc - 1) commit(&ctl.a_empty);
                             };
                             if (!two && i < nc) dp();
                             if (i > 0) {
@@ -724,23 +735,23 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                                 if (!need(smem_u32(&ctl.ds_full[cp & 1]), (cp >> 1) & 1)) break;
                                 if (two && i < nc && !need(smem_u32(&ctl.s_full[c & 1]), (c >> 1) & 1)) break;
                                 tc_fence_after();
-                                const uint32_t ds = tmem + (!two && !(i & 1) ? T_A0 : T_DP);
+                                const uint32_t ds = tm + (!two && !(i & 1) ? T_A0 : T_DP);
                                 const uint32_t b = sbase + L::B0 + sp * L::TILE;
-                                accumulate(tmem + T_A1, ds, b, 0, i == 1);
-                                accumulate(tmem + T_A1, ds, b, 1, false);
-                                mma_commit(smem_u32(&ctl.b0_empty[sp]));
+                                accumulate(tm + T_A1, ds, b, 0, i == 1);
+                                accumulate(tm + T_A1, ds, b, 1, false);
+                                commit(&ctl.b0_empty[sp]);
                             }
                             if (i == nc) break;
                             if (two) dp();
                         }
                     }
                     if (!ok) break;
-                    mma_commit(smem_u32(&ctl.acc_full));
+                    commit(&ctl.acc_full);
                     ++n_seq;
                 }
                 // every MMA this thread issued has completed before the tensor memory is released
-                mma_commit(smem_u32(&ctl.drain[warp >> 1]));
-                wait_bar_drain(smem_u32(&ctl.drain[warp >> 1]), 0, wlim);
+                commit(&ctl.drain[first_role ? 0 : 1]);
+                wait_bar_drain(smem_u32(&ctl.drain[first_role ? 0 : 1]), 0, wlim);
             }
             __syncwarp();
         }

@@ -319,6 +319,16 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 // no-op when this grid was launched without the programmatic attribute).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// ---------------------------------------------------------------- one lane of a converged warp
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // ---------------------------------------------------------------- register split
 
 // Per-warpgroup register budget (setmaxnreg; every warp of the warpgroup
