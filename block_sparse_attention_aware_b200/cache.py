@@ -24,7 +24,7 @@ import torch
 
 from . import fvattn
 from .fvattn import _check
-from .train import _on
+from .train import _check_call, _need, _need_workspace, _on
 
 EXPORTED = ("fvattn_cache_append", "fvattn_cache_attn_parts", "fvattn_cache_attn_workspace_size",
             "fvattn_cache_attn")
@@ -78,7 +78,7 @@ def rotation_table(D: int, axes: Sequence[int], rows: int, base: float = 10000.0
 
 
 def _vector(name, t, n, dev, dtype=I32):
-    if t is None or t.dtype != dtype or t.device != dev or t.shape != (n,) or not t.is_contiguous():
+    if t is None or t.dtype is not dtype or t.device != dev or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape ({n},) on {dev}")
 
 
@@ -105,22 +105,29 @@ class PagedCache:
         return cls(torch.empty(shape, dtype=BF16, device=device), torch.empty(shape, dtype=BF16, device=device))
 
     def _rows(self, name, t, rows, heads):
-        """A [rows, heads, D] view whose rows may lie apart (a slice of a wider projection)."""
-        if t is None or t.dtype != BF16 or t.device != self.device or t.dim() != 3 or \
-                (rows is not None and t.shape[0] != rows) or (heads is not None and t.shape[1] != heads) or \
-                t.shape[1] < 1 or t.shape[2] != self.D:
+        """(rows, heads, row stride) of a [rows, heads, D] view whose rows may lie apart (a slice of a wider
+        projection)."""
+        if t is None:
+            raise ValueError(f"{name} is required")
+        shape = t.shape
+        if t.dtype is not BF16 or t.device != self.device or len(shape) != 3 or \
+                (rows is not None and shape[0] != rows) or (heads is not None and shape[1] != heads) or \
+                shape[1] < 1 or shape[2] != self.D:
             raise ValueError(f"{name}: expected a bf16 tensor [{'rows' if rows is None else rows}, "
-                             f"{'heads' if heads is None else heads}, {self.D}] on {self.device}")
-        row = t.shape[1] * self.D
-        stride = t.stride(0) if t.shape[0] > 1 else row
-        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.D) or stride < row or stride % 8:
+                             f"{'heads' if heads is None else heads}, {self.D}] on {self.device}, got {t.dtype} "
+                             f"{tuple(shape)} on {t.device}")
+        row = shape[1] * self.D
+        sr, sh, sd = t.stride()
+        if shape[0] <= 1:
+            sr = row
+        if sd != 1 or (shape[1] > 1 and sh != self.D) or sr < row or sr % 8:
             raise ValueError(f"{name}: a row's heads must be contiguous and rows a multiple of 8 elements apart, "
                              f"got strides {t.stride()}")
-        return stride
+        return shape[0], shape[1], sr
 
     def _table(self, table):
-        if table.dtype != I32 or table.device != self.device or table.dim() != 2 or not table.is_contiguous() or \
-                table.shape[0] < 1 or table.shape[1] < 1:
+        if table is None or table.dtype is not I32 or table.device != self.device or table.dim() != 2 or \
+                not table.is_contiguous() or table.numel() < 1:
             raise ValueError(f"table: expected a contiguous int32 tensor [B, width] on {self.device}")
         return table.shape
 
@@ -136,16 +143,17 @@ class PagedCache:
         _vector("lens", lens, B, self.device)
         if cu is not None:
             _vector("cu", cu, B + 1, self.device)
-        ks = self._rows("k", k, None, self.Hkv)
-        rows = k.shape[0]
-        vs = self._rows("v", v, rows, self.Hkv)
+        rows, _, ks = self._rows("k", k, None, self.Hkv)
+        _, _, vs = self._rows("v", v, rows, self.Hkv)
         if cu is None and rows < B:
             raise ValueError(f"{rows} rows for {B} sequences: without cu, row b is sequence b's token")
         qs = qos = hq = 0
         if q is not None:
-            qs, hq = self._rows("q", q, rows, None), q.shape[1]
+            _, hq, qs = self._rows("q", q, rows, None)
             if q_out is not None:
-                qos = self._rows("q_out", q_out, rows, hq)
+                _, _, qos = self._rows("q_out", q_out, rows, hq)
+                if q_out.data_ptr() == q.data_ptr() and qos != qs:
+                    raise ValueError("q_out starts where q does, with other strides")
         elif q_out is not None:
             raise ValueError("q_out without q")
         r = None
@@ -156,7 +164,7 @@ class PagedCache:
                 raise ValueError(f"rot: expected a contiguous fp32 tensor [positions, {self.D}] on {self.device}")
             if not 1 <= len(axes) <= 3 or min(axes) < 0 or sum(axes) != self.D // 2:
                 raise ValueError(f"axes {axes}: one to three counts adding up to {self.D // 2} pairs")
-            if pos is None or pos.dtype != I32 or pos.device != self.device or tuple(pos.shape) != (rows, len(axes)) or \
+            if pos is None or pos.dtype != I32 or pos.device != self.device or pos.shape != (rows, len(axes)) or \
                     not pos.is_contiguous():
                 raise ValueError(f"pos: expected a contiguous int32 tensor ({rows}, {len(axes)}) on {self.device}")
             r = _Rotation(rot.data_ptr(), rot.shape[0], len(axes), (ctypes.c_int * 3)(*axes), pos.data_ptr(), bool(halves))
@@ -167,12 +175,15 @@ class PagedCache:
             if q is not None and q_out is None:
                 q_out = torch.empty((rows, hq, self.D), dtype=BF16, device=self.device)
                 qos = hq * self.D
-            _check("fvattn_cache_append",
-                   L.fvattn_cache_append(ctypes.byref(self._c), B, rows, None if cu is None else cu.data_ptr(),
-                                         lens.data_ptr(), table.data_ptr(), width, k.data_ptr(), ks, v.data_ptr(), vs,
-                                         None if q is None else q.data_ptr(), qs, hq,
-                                         None if q is None else q_out.data_ptr(), qos,
-                                         None if r is None else ctypes.byref(r), s))
+            if rows == 0:
+                return q_out
+            rc = L.fvattn_cache_append(ctypes.byref(self._c), B, rows, None if cu is None else cu.data_ptr(),
+                                       lens.data_ptr(), table.data_ptr(), width, k.data_ptr(), ks, v.data_ptr(), vs,
+                                       None if q is None else q.data_ptr(), qs, hq,
+                                       None if q is None else q_out.data_ptr(), qos,
+                                       None if r is None else ctypes.byref(r), s)
+            if rc:
+                _check("fvattn_cache_append", rc)
         return q_out
 
     def attend_workspace(self, B: int, Hq: int, longest: int) -> torch.Tensor:
@@ -189,31 +200,33 @@ class PagedCache:
         multiple of Hkv.  `longest`: no sequence is longer (default: what the
         table can hold; a nearer bound splits better)."""
         B, width = self._table(table)
-        qs = self._rows("q", q, B, None)
-        hq = q.shape[1]
+        _, hq, qs = self._rows("q", q, B, None)
         if hq % self.Hkv:
             raise ValueError(f"{hq} query heads do not divide over {self.Hkv} key heads")
         _vector("lens", lens, B, self.device)
         longest = width * self.page if longest is None else int(longest)
-        for name, t, shape, dtype in (("out", out, q.shape, BF16), ("lse", lse, (B, hq), F32)):
-            if t is not None and (t.dtype != dtype or t.device != self.device or t.shape != shape or not t.is_contiguous()):
-                raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {self.device}")
+        if out is not None:
+            _need("out", out, q.shape, BF16, self.device)
+        if lse is not None:
+            _need("lse", lse, (B, hq), F32, self.device)
+        if workspace is not None:
+            _need_workspace(workspace, self.device)
+        scale = 1.0 / math.sqrt(self.D) if scale is None else float(scale)
+        if not (0.0 < scale < math.inf) or longest < 0:
+            raise ValueError(f"scale {scale}, longest {longest}: expected a positive finite scale and longest >= 0")
         L = load()
         with _on(self.device, stream) as s:
-            need = L.fvattn_cache_attn_workspace_size(B, hq, self.Hkv, self.D, longest)
             if workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-            elif workspace.dtype != torch.uint8 or workspace.device != self.device or not workspace.is_contiguous() or \
-                    workspace.numel() < need:
-                raise ValueError(f"workspace: expected a contiguous uint8 tensor of at least {need} elements on {self.device}")
+                need = L.fvattn_cache_attn_workspace_size(B, hq, self.Hkv, self.D, longest)
+                workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
             if out is None:
                 out = torch.empty((B, hq, self.D), dtype=BF16, device=self.device)
             if lse is None:
                 lse = torch.empty((B, hq), dtype=F32, device=self.device)
-            _check("fvattn_cache_attn",
-                   L.fvattn_cache_attn(ctypes.byref(self._c), B, hq, q.data_ptr(), qs, table.data_ptr(), width,
-                                       lens.data_ptr(), longest,
-                                       1.0 / math.sqrt(self.D) if scale is None else float(scale), out.data_ptr(),
-                                       lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
-                                       0 if workspace is None else workspace.numel(), s))
+            rc = L.fvattn_cache_attn(ctypes.byref(self._c), B, hq, q.data_ptr(), qs, table.data_ptr(), width,
+                                     lens.data_ptr(), longest, scale, out.data_ptr(), lse.data_ptr(),
+                                     workspace.data_ptr(), workspace.numel(), s)
+            if rc:
+                _check_call("fvattn_cache_attn", rc, workspace,
+                            lambda: L.fvattn_cache_attn_workspace_size(B, hq, self.Hkv, self.D, longest))
         return out, lse

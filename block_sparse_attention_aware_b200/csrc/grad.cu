@@ -52,6 +52,7 @@
 // each row sees only the columns of blocks that its own block is paired with.
 #include <cuda.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -227,6 +228,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
+    pdl_wait();              // the lists, the statistics, and for KV the query pass's delta
+    pdl_launch_dependents();
 
     if (warp >= 4) {
         regs_inc<GRAD_HIGH>();
@@ -769,7 +772,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
 // per 8 rows; 16 bytes of O and dO a lane), the former -inf for padding rows
 // and rows that keep no block, so that their P is 0; and for each 8 rows the
 // largest |O|^2 and the sum of |v|^2.  The others: one warp
-// per (b, h, query block) writes its kv list as a bit row.
+// per (b, h, query block) writes its kv list as a bit row; those of the first
+// head write the blocks' extents.
 template <int D>
 __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, int nwords,
                                                         const uint4* __restrict__ o, const uint4* __restrict__ dout,
@@ -778,8 +782,10 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, 
                                                         const int32_t* __restrict__ kv_idx,
                                                         const int32_t* __restrict__ kv_cnt,
                                                         float* __restrict__ nlse2, float* __restrict__ ndelta,
-                                                        float2* __restrict__ norms, uint32_t* __restrict__ bits) {
+                                                        float2* __restrict__ norms, uint32_t* __restrict__ bits,
+                                                        int32_t* __restrict__ ext) {
     extern __shared__ uint32_t gp_bits[];   // [8][nwords]
+    pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (static_cast<int>(blockIdx.x) < stat_blocks) {
         constexpr int LPR = D / 8;           // lanes a row
@@ -835,6 +841,7 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, 
     }
     const long long unit = (static_cast<long long>(blockIdx.x) - stat_blocks) * 8 + warp;
     if (unit >= static_cast<long long>(g.B) * g.H * g.nb) return;
+    if (unit < g.nb && lane == 0) ext[unit] = grad_extent(g, static_cast<int>(unit));
     uint32_t* mine = gp_bits + warp * nwords;
     for (int i = lane; i < nwords; i += 32) mine[i] = 0u;
     __syncwarp();
@@ -866,6 +873,8 @@ __global__ void __launch_bounds__(256) grad_lists_kernel(Geo g, int G, int ngrou
                                                          uint32_t* __restrict__ ulq, int32_t* __restrict__ cntq,
                                                          uint32_t* __restrict__ ulk, int32_t* __restrict__ cntk) {
     const int lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();
     const long long units = static_cast<long long>(g.B) * g.H * ngroups;
     long long unit = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const bool keys = unit >= units;
@@ -929,6 +938,8 @@ __global__ void __launch_bounds__(256) grad_order_kernel(Geo g, int G, int ngrou
                                                          int32_t* __restrict__ ordk, int* __restrict__ counters) {
     const int BH = g.B * g.H, nb = g.nb;
     __shared__ float part[256];
+    pdl_launch_dependents();
+    pdl_wait();
     extern __shared__ int go_start[];   // [nb + 1]
     const int dir = static_cast<int>(blockIdx.x) / BH, bh = static_cast<int>(blockIdx.x) - dir * BH;
     const int32_t* cnt = (dir ? cntk : cntq) + static_cast<long long>(bh) * ngroups;
@@ -980,12 +991,6 @@ __global__ void __launch_bounds__(256) grad_order_kernel(Geo g, int G, int ngrou
     }
 }
 
-// Every block's real extent.
-__global__ void __launch_bounds__(256) grad_extent_kernel(Geo g, int32_t* __restrict__ ext) {
-    const int b = blockIdx.x * 256 + threadIdx.x;
-    if (b < g.nb) ext[b] = grad_extent(g, b);
-}
-
 // ------------------------------------------------------------------ host side
 
 struct GradWs {
@@ -1017,21 +1022,41 @@ static GradWs grad_ws(const fvattn_geom& g) {
     return w;
 }
 
+// A launch that may begin while the stream's kernel before it ends; it waits
+// for that one's results itself (pdl_wait).
+template <class... P, class... A>
+static int launch_after(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA;
+}
+
 template <int D, bool KV>
 static int launch_grad(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
-                       const GradArgs& args, int grid, cudaStream_t s) {
+                       const GradArgs& args, int grid, int dev, cudaStream_t s) {
     using L = GradSmem<D>;
-    if (cudaFuncSetAttribute(grad_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(L::ALLOC)) != cudaSuccess)
-        return FVATTN_ERR_CUDA;
-    // setmaxnreg waits for ever for registers that the CTA was not launched with
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, grad_kernel<D, KV>) != cudaSuccess) return FVATTN_ERR_CUDA;
-    if (static_cast<long long>(fa.numRegs) * GRAD_THREADS < 128ll * (GRAD_LOW + GRAD_GROUPS * GRAD_HIGH))
-        return FVATTN_ERR_UNSUPPORTED;
-    grad_kernel<D, KV><<<grid, GRAD_THREADS, L::ALLOC, s>>>(a0, a1, b0, b1, args);
-    FV_CHECK_LAUNCH();
-    return FVATTN_OK;
+    static std::atomic<unsigned long long> ready{0};   // devices on which the kernel has its shared memory
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if ((ready.load(std::memory_order_relaxed) & bit) == 0ull) {
+        if (cudaFuncSetAttribute(grad_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(L::ALLOC)) != cudaSuccess)
+            return FVATTN_ERR_CUDA;
+        // setmaxnreg waits for ever for registers that the CTA was not launched with
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, grad_kernel<D, KV>) != cudaSuccess) return FVATTN_ERR_CUDA;
+        if (static_cast<long long>(fa.numRegs) * GRAD_THREADS < 128ll * (GRAD_LOW + GRAD_GROUPS * GRAD_HIGH))
+            return FVATTN_ERR_UNSUPPORTED;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return launch_after(grad_kernel<D, KV>, static_cast<unsigned>(grid), GRAD_THREADS, L::ALLOC, s, a0, a1, b0, b1, args);
 }
 
 template <int D>
@@ -1069,16 +1094,14 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
     const int bit_blocks = static_cast<int>((static_cast<long long>(BH) * g.nb + 7) / 8);
     grad_prep_kernel<D><<<stat_blocks + bit_blocks, 256, sizeof(uint32_t) * 8 * wl.nwords, s>>>(
         g, stat_blocks, wl.nwords, static_cast<const uint4*>(o_t), static_cast<const uint4*>(do_t),
-        static_cast<const uint4*>(v_t), lse, kv_idx, kv_cnt, nlse2, ndelta, norms, bits);
+        static_cast<const uint4*>(v_t), lse, kv_idx, kv_cnt, nlse2, ndelta, norms, bits, ext);
     FV_CHECK_LAUNCH();
-    grad_extent_kernel<<<(g.nb + 255) / 256, 256, 0, s>>>(g, ext);
-    FV_CHECK_LAUNCH();
-    grad_lists_kernel<<<static_cast<unsigned>((2ll * BH * wl.ngroups + 7) / 8), 256, 0, s>>>(
-        g, wl.G, wl.ngroups, wl.nwords, bits, ulq, cntq, ulk, cntk);
-    FV_CHECK_LAUNCH();
-    grad_order_kernel<<<2 * BH, 256, sizeof(int) * (g.nb + 1), s>>>(g, wl.G, wl.ngroups, norms, cntq, cntk, ordq,
-                                                                    ordk, counters);
-    FV_CHECK_LAUNCH();
+    int rc = launch_after(grad_lists_kernel, static_cast<unsigned>((2ll * BH * wl.ngroups + 7) / 8), 256, 0, s, g, wl.G,
+                          wl.ngroups, wl.nwords, bits, ulq, cntq, ulk, cntk);
+    if (rc != FVATTN_OK) return rc;
+    rc = launch_after(grad_order_kernel, 2 * BH, 256, sizeof(int) * (g.nb + 1), s, g, wl.G, wl.ngroups, norms, cntq, cntk,
+                      ordq, ordk, counters);
+    if (rc != FVATTN_OK) return rc;
 
     GradArgs a;
     a.g = g;
@@ -1099,7 +1122,7 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
     a.counter = counters;
     a.out0 = static_cast<__nv_bfloat16*>(dq_t);
     a.out1 = nullptr;
-    int rc = launch_grad<D, false>(tq, tdo, tk, tv, a, grid, s);
+    rc = launch_grad<D, false>(tq, tdo, tk, tv, a, grid, dev, s);
     if (rc != FVATTN_OK) return rc;
     a.ul = ulk;
     a.cnt = cntk;
@@ -1107,7 +1130,7 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
     a.counter = counters + 1;
     a.out0 = static_cast<__nv_bfloat16*>(dv_t);
     a.out1 = static_cast<__nv_bfloat16*>(dk_t);
-    return launch_grad<D, true>(tk, tv, tq, tdo, a, grid, s);
+    return launch_grad<D, true>(tk, tv, tq, tdo, a, grid, dev, s);
 }
 
 }  // namespace fv

@@ -18,7 +18,7 @@ from typing import Optional
 import torch
 
 from . import fvattn
-from .fvattn import Geom, _check, _expect, _ptr, _raster, _tiled
+from .fvattn import Geom, _check, _raster
 
 EXPORTED = ("fvattn_sparse_attn_lse", "fvattn_sparse_attn_bwd_workspace_size", "fvattn_sparse_attn_bwd")
 
@@ -42,39 +42,67 @@ def load():
     return _lib
 
 
-@contextlib.contextmanager
-def _on(device, stream):
+class _on:
     """Run a call on `device` and on `stream` (None: that device's current
-    stream); yields the stream handle.  Outputs and workspaces made inside
-    belong to that stream."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        else:
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+    stream); the value is the stream handle.  Outputs and workspaces made
+    inside belong to that stream."""
+    __slots__ = ("device", "stream", "outer")
+
+    def __init__(self, device: torch.device, stream):
+        self.device, self.stream, self.outer = device, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is None and torch.cuda.current_device() == self.device.index:   # nothing to switch
+            return torch.cuda.current_stream().cuda_stream
+        self.outer = contextlib.ExitStack()
+        self.outer.enter_context(torch.cuda.device(self.device))
+        stream = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
+        if stream.device != self.device:
+            self.outer.close()
+            raise ValueError(f"stream: on {stream.device}, the call's tensors are on {self.device}")
+        self.outer.enter_context(torch.cuda.stream(stream))
+        return stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.outer is not None:
+            self.outer.close()
 
 
-def _same_device(first: torch.Tensor, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name}: on {t.device}, the call's first tensor is on {first.device}")
-
-
-def _need(name: str, t, shape, dtype):
+def _device(name: str, t) -> torch.device:
+    """The device of a call, that of its first tensor."""
     if t is None:
         raise ValueError(f"{name} is required")
-    _expect(name, t, shape, dtype)
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return t.device
 
 
-def _expect_workspace(ws: torch.Tensor, size: int):
-    if not ws.is_cuda or not ws.is_contiguous() or ws.dtype != torch.uint8 or ws.numel() < size:
-        raise ValueError(f"workspace: expected a contiguous CUDA uint8 tensor of at least {size} elements")
+def _need(name: str, t, shape, dtype, device):
+    """The kernels read and write dense buffers of exactly this shape."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
 
 
-def _expect_lists(g: Geom, kv_idx, kv_cnt):
-    _need("kv_idx", kv_idx, (g.B, g.H, g.nb, g.nb), torch.int32)
-    _need("kv_cnt", kv_cnt, (g.B, g.H, g.nb), torch.int32)
+def _check_call(what: str, rc: int, workspace, size):
+    """Raise for a call's error; `size()` is the workspace that it needed."""
+    if rc == fvattn.ERR_INVALID and workspace is not None and workspace.numel() < size():
+        raise ValueError(f"workspace: expected at least {size()} bytes, got {workspace.numel()}")
+    _check(what, rc)
+
+
+def _need_workspace(ws, device):
+    if ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous uint8 tensor on {device}")
+
+
+def _scale(g: Geom, scale) -> float:
+    scale = 1.0 / math.sqrt(g.D) if scale is None else float(scale)
+    if not (0.0 < scale < math.inf):
+        raise ValueError(f"scale: expected a positive finite number, got {scale}")
+    return scale
 
 
 def sparse_attn_lse(g: Geom, qt, kt, vt, kv_idx, kv_cnt, scale: Optional[float] = None,
@@ -82,26 +110,35 @@ def sparse_attn_lse(g: Geom, qt, kt, vt, kv_idx, kv_cnt, scale: Optional[float] 
                     sm_stats: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
     """fvattn_sparse_attn_lse: (tiled O, lse [B, H, Npad] fp32).  A row with
     kv_cnt = 0 gets O = 0, lse = -inf.  `workspace` as fvattn.attn_workspace."""
+    dev = _device("qt", qt)
+    B, H, nb, Npad = g.B, g.H, g.nb, g.Npad
+    tiled = (B, H, Npad, g.D)
     for name, t in (("qt", qt), ("kt", kt), ("vt", vt)):
-        _need(name, t, _tiled(g), torch.bfloat16)
-    _expect_lists(g, kv_idx, kv_cnt)
-    _expect("out", out, _tiled(g), torch.bfloat16)
-    _expect("lse", lse, (g.B, g.H, g.Npad), torch.float32)
-    _same_device(qt, kt=kt, vt=vt, kv_idx=kv_idx, kv_cnt=kv_cnt, out=out, lse=lse, sm_stats=sm_stats,
-                 workspace=workspace)
+        _need(name, t, tiled, torch.bfloat16, dev)
+    _need("kv_idx", kv_idx, (B, H, nb, nb), torch.int32, dev)
+    _need("kv_cnt", kv_cnt, (B, H, nb), torch.int32, dev)
+    if out is not None:
+        _need("out", out, tiled, torch.bfloat16, dev)
+        if out.data_ptr() in (qt.data_ptr(), kt.data_ptr(), vt.data_ptr()):
+            raise ValueError("out must not be an input")
+    if lse is not None:
+        _need("lse", lse, (B, H, Npad), torch.float32, dev)
     if sm_stats is not None:
-        _expect("sm_stats", sm_stats, (2 * fvattn.num_sms(),), torch.int64)
-    L = load()
+        _need("sm_stats", sm_stats, (2 * fvattn.num_sms(),), torch.int64, dev)
     if workspace is not None:
-        _expect_workspace(workspace, L.fvattn_attn_workspace_size(ctypes.byref(g)))
-    with _on(qt.device, stream) as s:
-        out = fvattn.tiled_empty(g, qt.device) if out is None else out
-        lse = torch.empty((g.B, g.H, g.Npad), dtype=torch.float32, device=qt.device) if lse is None else lse
-        workspace = fvattn.attn_workspace(g, qt.device) if workspace is None else workspace
-        _check("fvattn_sparse_attn_lse",
-               L.fvattn_sparse_attn_lse(ctypes.byref(g), _ptr(qt), _ptr(kt), _ptr(vt), _ptr(kv_idx), _ptr(kv_cnt),
-                                        1.0 / math.sqrt(g.D) if scale is None else float(scale), _ptr(out), _ptr(lse),
-                                        _ptr(sm_stats), _ptr(workspace), workspace.numel(), s))
+        _need_workspace(workspace, dev)
+    scale = _scale(g, scale)
+    L = load()
+    with _on(dev, stream) as s:
+        out = torch.empty(tiled, dtype=torch.bfloat16, device=dev) if out is None else out
+        lse = torch.empty((B, H, Npad), dtype=torch.float32, device=dev) if lse is None else lse
+        workspace = fvattn.attn_workspace(g, dev) if workspace is None else workspace
+        rc = L.fvattn_sparse_attn_lse(ctypes.byref(g), qt.data_ptr(), kt.data_ptr(), vt.data_ptr(), kv_idx.data_ptr(),
+                                      kv_cnt.data_ptr(), scale, out.data_ptr(), lse.data_ptr(),
+                                      None if sm_stats is None else sm_stats.data_ptr(), workspace.data_ptr(),
+                                      workspace.numel(), s)
+    if rc:
+        _check_call("fvattn_sparse_attn_lse", rc, workspace, lambda: L.fvattn_attn_workspace_size(ctypes.byref(g)))
     return out, lse
 
 
@@ -118,29 +155,36 @@ def sparse_attn_bwd(g: Geom, qt, kt, vt, ot, dot, lse, kv_idx, kv_cnt, scale: Op
     """fvattn_sparse_attn_bwd: tiled (dQ, dK, dV) from the tensors of a
     sparse_attn_lse call and the tiled gradient `dot` of its output, whose
     padding rows are zero as fvattn.reorder writes them."""
+    dev = _device("qt", qt)
+    B, H, nb, Npad = g.B, g.H, g.nb, g.Npad
+    tiled = (B, H, Npad, g.D)
     for name, t in (("qt", qt), ("kt", kt), ("vt", vt), ("ot", ot), ("dot", dot)):
-        _need(name, t, _tiled(g), torch.bfloat16)
-    _need("lse", lse, (g.B, g.H, g.Npad), torch.float32)
-    _expect_lists(g, kv_idx, kv_cnt)
-    inputs = [t.data_ptr() for t in (qt, kt, vt, ot, dot)]
-    outputs = [t.data_ptr() for t in (dq, dk, dv) if t is not None]
-    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
-        _expect(name, t, _tiled(g), torch.bfloat16)
-    if len(set(outputs)) < len(outputs) or set(outputs) & set(inputs):
-        raise ValueError("dq, dk and dv must be distinct buffers and no input")
-    _same_device(qt, kt=kt, vt=vt, ot=ot, dot=dot, lse=lse, kv_idx=kv_idx, kv_cnt=kv_cnt, dq=dq, dk=dk, dv=dv,
-                 workspace=workspace)
-    L = load()
+        _need(name, t, tiled, torch.bfloat16, dev)
+    _need("lse", lse, (B, H, Npad), torch.float32, dev)
+    _need("kv_idx", kv_idx, (B, H, nb, nb), torch.int32, dev)
+    _need("kv_cnt", kv_cnt, (B, H, nb), torch.int32, dev)
+    outputs = [t for t in (dq, dk, dv) if t is not None]
+    if outputs:
+        for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+            if t is not None:
+                _need(name, t, tiled, torch.bfloat16, dev)
+        places = {t.data_ptr() for t in outputs}
+        if len(places) < len(outputs) or places & {t.data_ptr() for t in (qt, kt, vt, ot, dot)}:
+            raise ValueError("dq, dk and dv must be distinct buffers and no input")
     if workspace is not None:
-        _expect_workspace(workspace, L.fvattn_sparse_attn_bwd_workspace_size(ctypes.byref(g)))
-    with _on(qt.device, stream) as s:
-        dq, dk, dv = (fvattn.tiled_empty(g, qt.device) if t is None else t for t in (dq, dk, dv))
-        workspace = bwd_workspace(g, qt.device) if workspace is None else workspace
-        _check("fvattn_sparse_attn_bwd",
-               L.fvattn_sparse_attn_bwd(ctypes.byref(g), _ptr(qt), _ptr(kt), _ptr(vt), _ptr(ot), _ptr(dot), _ptr(lse),
-                                        _ptr(kv_idx), _ptr(kv_cnt),
-                                        1.0 / math.sqrt(g.D) if scale is None else float(scale), _ptr(dq), _ptr(dk),
-                                        _ptr(dv), _ptr(workspace), workspace.numel(), s))
+        _need_workspace(workspace, dev)
+    scale = _scale(g, scale)
+    L = load()
+    with _on(dev, stream) as s:
+        dq, dk, dv = (torch.empty(tiled, dtype=torch.bfloat16, device=dev) if t is None else t for t in (dq, dk, dv))
+        workspace = bwd_workspace(g, dev) if workspace is None else workspace
+        rc = L.fvattn_sparse_attn_bwd(ctypes.byref(g), qt.data_ptr(), kt.data_ptr(), vt.data_ptr(), ot.data_ptr(),
+                                      dot.data_ptr(), lse.data_ptr(), kv_idx.data_ptr(), kv_cnt.data_ptr(), scale,
+                                      dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+                                      workspace.numel(), s)
+    if rc:
+        _check_call("fvattn_sparse_attn_bwd", rc, workspace,
+                    lambda: L.fvattn_sparse_attn_bwd_workspace_size(ctypes.byref(g)))
     return dq, dk, dv
 
 
@@ -174,10 +218,11 @@ def attention(g: Geom, q, k, v, kv_idx, kv_cnt, scale: Optional[float] = None, o
     bf16) on given kv lists: raster O.  The lists are kept for the backward
     pass, and must hold the same values then.  `order`: the table of a
     geometry made with fvattn.with_order, kept alive with the call."""
+    dev = _device("q", q)
     for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(name, t, _raster(g), torch.bfloat16)
-    _expect_lists(g, kv_idx, kv_cnt)
-    _same_device(q, k=k, v=v, kv_idx=kv_idx, kv_cnt=kv_cnt)
+        _need(name, t, _raster(g), torch.bfloat16, dev)
+    _need("kv_idx", kv_idx, (g.B, g.H, g.nb, g.nb), torch.int32, dev)
+    _need("kv_cnt", kv_cnt, (g.B, g.H, g.nb), torch.int32, dev)
     if g.order and order is None:
         raise ValueError("a geometry with a block order needs its table: pass order=")
     return _Attention.apply(q, k, v, g, order, None, kv_idx, kv_cnt, scale)
@@ -203,9 +248,9 @@ class TrainLayer:
         return fvattn.reorder_route(self.g, q.detach(), k.detach(), self.p, self.k, self.scale)
 
     def __call__(self, q, k, v) -> torch.Tensor:
+        dev = _device("q", q)
         for name, t in (("q", q), ("k", k), ("v", v)):
-            _need(name, t, _raster(self.g), torch.bfloat16)
-        _same_device(q, k=k, v=v)
+            _need(name, t, _raster(self.g), torch.bfloat16, dev)
         with torch.cuda.device(q.device):
             qt, kt, routed = self.route(q, k)
         return _Attention.apply(q, k, v, self.g, self.order_table, (qt, kt), routed.kv_idx, routed.kv_cnt, self.scale)
