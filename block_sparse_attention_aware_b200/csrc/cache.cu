@@ -6,17 +6,22 @@
 //
 // Attention of one token reads each cached key and value once for a handful
 // of multiply-adds: bound by memory too, so the kernel's whole form follows
-// from keeping enough of the cache in flight.  One CTA takes one key head of
-// one sequence and a part of its tokens: a producer warp TMA-loads 64-token
-// tiles of K and V through the page table into a ring of shared memory, four
-// warps take 16 tokens of a tile each and keep an online softmax of their own
-// (running maximum, sum and O in registers), and the four are joined at the
-// end.  The heads that share a key head ride along in one product:
+// from keeping enough of the cache in flight, on every SM until the end.  The
+// tokens of a sequence are split into parts of one size; an item is a part of
+// one key head of one sequence, and 2 persistent CTAs an SM take the items
+// that exist (from the lengths, on the device) in turn.  In a CTA a producer
+// warp TMA-loads 64-token tiles of K and V through the page table into a ring
+// of shared memory and runs on into the next item; four warps take 16 tokens
+// of a tile each and keep an online softmax of their own (running maximum,
+// sum and O in registers), and the four are joined at the item's end.  The
+// heads that share a key head ride along in one product:
 //   S^T [16 tokens x 8 heads] = K Q^T,  O^T [D x 8 heads] += V^T P^T
 // with mma.sync.m16n8k16 (8 heads an N tile; a tcgen05 tile would have 128
-// rows of which one to sixteen hold a query).  Long sequences are split into
-// parts, whose (maximum, sum, O) a second small kernel joins in part order.
+// rows of which one to sixteen hold a query).  The parts' (maximum, sum, O)
+// are joined in part order by a second small kernel.
 #include <cuda.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "fvattn_cache.h"
@@ -147,21 +152,26 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
 // ------------------------------------------------------------------ attention of one token
 
 constexpr int DEC_TILE = 64;            // tokens a ring stage
-constexpr int DEC_WARPS = 4;            // arithmetic warps, 16 tokens of a tile each
+constexpr int DEC_WARPS = 4;            // arithmetic warps: two take a tile, 32 tokens each
 constexpr int DEC_THREADS = 32 * (DEC_WARPS + 1);
 constexpr int DEC_CTAS = 2;             // CTAs an SM
-constexpr int DEC_MAX_PARTS = 128;
+constexpr int DEC_MAX_PARTS = 256;
 
 template <int D>
 struct DecSmem {
     static constexpr uint32_t TILE = DEC_TILE * D * 2u;          // D/64 halves of 8 KB, 128-byte swizzled rows
     static constexpr int STAGES = D == 128 ? 3 : 6;              // 96 KB a CTA
-    static constexpr uint32_t K = 0, V = STAGES * TILE, BARS = 2 * STAGES * TILE;
-    static constexpr uint32_t TOTAL = BARS + 16u * STAGES + 16u;
+    static constexpr uint32_t K = 0, V = STAGES * TILE;
+    static constexpr uint32_t JO = 2 * STAGES * TILE;            // [warp][8 heads][64] a piece of the four warps' O
+    static constexpr uint32_t JM = JO + DEC_WARPS * 8 * 64 * 4u; // [warp][8] maximum, then sum
+    static constexpr uint32_t BARS = JM + 2 * DEC_WARPS * 8 * 4u;
+    static constexpr uint32_t ITEM = BARS + 8u * (3 * STAGES + 6);   // 2 x 4 words
+    static constexpr uint32_t TOTAL = ITEM + 32u;
+    static_assert(DEC_CTAS * (TOTAL + 1024u) <= 233472u, "shared memory of an SM");
 };
 
 struct DecArgs {
-    int Hq, Hkv, group, gchunks, page, pages, width, tokens, parts;
+    int B, Hq, Hkv, group, gchunks, page, pages, width, tokens, parts;
     long long longest, q_stride;
     const __nv_bfloat16* q;
     const int32_t *table, *lens;
@@ -216,98 +226,158 @@ __global__ void __launch_bounds__(DEC_THREADS, DEC_CTAS)
     __shared__ int s_abort;
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int part = blockIdx.x;
-    const int hk = blockIdx.y / a.gchunks, gc = blockIdx.y - hk * a.gchunks;
-    const int b = blockIdx.z;
-    const int head0 = hk * a.group + gc * 16;                 // first query head of this CTA
-    const int nheads = min(16, a.group - gc * 16);
     pdl_launch_dependents();
-    const int len = cache_len(a, b);
-    const int t0 = part * a.tokens;
-    const int t1 = min(len, t0 + a.tokens);
-    if (t1 <= t0) {
-        // an empty part is not read by the join; an unsplit empty sequence is answered here
-        if (a.parts == 1)
-            for (int i = threadIdx.x; i < nheads * D; i += DEC_THREADS) {
-                const long long at = static_cast<long long>(b) * a.Hq + head0 + i / D;
-                a.o[at * D + i % D] = __float2bfloat16(0.f);
-                if (a.lse && i % D == 0) a.lse[at] = -INFINITY;
-            }
-        return;
-    }
     if (sbase & 1023u) {   // the 128-byte swizzle needs 1024-byte aligned tiles
         if (threadIdx.x == 0) record_status(FVATTN_ERR_UNSUPPORTED);
         return;
     }
+    // Tile k is in stage k % NS and lands on full barrier k % NB.  NB is even: a barrier's tiles all belong to
+    // one pair of warps, which waits for each of its phases (with a barrier a stage it would miss every second
+    // one, and a wait on the parity would return for the phase two uses before).
+    constexpr int NB = 2 * NS;
     unsigned long long* full = reinterpret_cast<unsigned long long*>(smem + L::BARS);
-    unsigned long long* empty = full + NS;
+    unsigned long long* empty = full + NB;
+    unsigned long long* item_full = empty + NS;      // [2]
+    unsigned long long* item_empty = item_full + 2;  // [2]
+    unsigned long long* join_full = item_empty + 2;  // the warps' parts are in shared memory
+    unsigned long long* join_free = join_full + 1;   // and have been read
+    int* items = reinterpret_cast<int*>(smem + L::ITEM);   // [2]: sequence, head chunk, first token, past the last (-1: end)
     volatile int* abort_flag = &s_abort;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(smem_u32(full + s), 1);
-            mbar_init(smem_u32(empty + s), DEC_WARPS);
+        for (int s = 0; s < NB; ++s) mbar_init(smem_u32(full + s), 1);
+        for (int s = 0; s < NS; ++s) mbar_init(smem_u32(empty + s), DEC_WARPS / 2);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(item_full + s), 1);
+            mbar_init(smem_u32(item_empty + s), DEC_WARPS);
         }
+        mbar_init(smem_u32(join_full), DEC_WARPS);
+        mbar_init(smem_u32(join_free), DEC_WARPS);
         s_abort = 0;
         fence_mbar_init();
     }
     __syncthreads();
-    const int tiles = (t1 - t0 + DEC_TILE - 1) / DEC_TILE;
-
-    float o[NT][D / 16][4];
-    float m[NT][2], l[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][d][i] = 0.f;
-    }
+    const int HG = a.Hkv * a.gchunks;
 
     if (warp == DEC_WARPS) {
-        // =========================== producer
+        // =========================== producer: items, tiles
         const int box = min(a.page, DEC_TILE);           // rows a load
         const int boxes = DEC_TILE / box;
-        const int32_t* row = a.table + static_cast<long long>(b) * a.width;
-        int it = 0;
-        for (; it < tiles; ++it) {
-            const int st = it % NS;
-            const int tok = t0 + it * DEC_TILE + lane * box;
-            int pg = 0;
-            const bool mine = lane < boxes && tok < t1;
-            if (mine) {
-                pg = __ldg(row + tok / a.page);
+        int b0 = 0, len = 0, seq = 0;
+        uint32_t it = 0;
+        long long before = 0, incl = 0;                  // items of the sequences before b0; of b0 .. b0 + lane
+        auto chunk = [&]() {                             // the items of 32 sequences, one a lane
+            len = b0 + lane < a.B ? cache_len(a, b0 + lane) : 0;
+            long long n = (static_cast<long long>(len) + a.tokens - 1) / a.tokens;
+            if (a.parts == 1 && b0 + lane < a.B) n = 1;  // an empty sequence is answered here
+            incl = n * HG;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += y;
+            }
+        };
+        chunk();
+        bool ok = true;
+        for (long long j = blockIdx.x; ok; j += gridDim.x) {
+            long long total = __shfl_sync(0xffffffffu, incl, 31);
+            while (j >= before + total && b0 + 32 < a.B) {
+                before += total;
+                b0 += 32;
+                chunk();
+                total = __shfl_sync(0xffffffffu, incl, 31);
+            }
+            const bool end = j >= before + total;
+            // the first sequence whose items end after j
+            const int sel = end ? 0 : __ffs(static_cast<int>(__ballot_sync(0xffffffffu, j < before + incl))) - 1;
+            const long long upto = __shfl_sync(0xffffffffu, incl, sel > 0 ? sel - 1 : 0);
+            const long long local = j - before - (sel > 0 ? upto : 0);
+            const int b = b0 + sel, hg = static_cast<int>(local % HG);
+            const int t0 = static_cast<int>(local / HG) * a.tokens;
+            const int blen = __shfl_sync(0xffffffffu, len, sel);
+            const int t1 = blen - t0 > a.tokens ? t0 + a.tokens : blen;
+            const int slot = seq & 1;
+            if (!wait_warp(smem_u32(item_empty + slot), ((seq >> 1) & 1) ^ 1, abort_flag)) break;
+            if (lane == 0) {
+                items[slot * 4] = b;
+                items[slot * 4 + 1] = hg;
+                items[slot * 4 + 2] = t0;
+                items[slot * 4 + 3] = end ? -1 : t1;
+                mbar_arrive(smem_u32(item_full + slot));
+            }
+            if (end) break;
+            ++seq;
+            const int hk = hg / a.gchunks;
+            const int32_t* row = a.table + static_cast<long long>(b) * a.width;
+            // a lane's page of the tile at t; looked up a tile ahead of its use
+            auto page_of = [&](int t) {
+                const int tok = t + lane * box;
+                return lane < boxes && tok < t1 ? __ldg(row + tok / a.page) : 0;
+            };
+            int next = page_of(t0);
+            for (int t = t0; t < t1; t += DEC_TILE, ++it) {
+                const int st = it % NS;
+                const int tok = t + lane * box;
+                const bool mine = lane < boxes && tok < t1;
+                int pg = next;
+                if (t1 - t > DEC_TILE) next = page_of(t + DEC_TILE);
                 if (pg < 0 || pg >= a.pages) {
                     record_status(FVATTN_ERR_BOUNDS);
                     pg = 0;
                 }
-            }
-            if (!wait_warp(smem_u32(empty + st), ((it / NS) & 1) ^ 1, abort_flag)) break;
-            const int nbox = __popc(__ballot_sync(0xffffffffu, mine));
-            if (lane == 0) mbar_arrive_expect_tx(smem_u32(full + st), static_cast<uint32_t>(2 * nbox * box * D * 2));
-            __syncwarp();
-            if (mine) {
-                const int r = (pg * a.Hkv + hk) * a.page + tok % a.page;
-                const uint32_t off = st * L::TILE + static_cast<uint32_t>(lane * box) * 128u;
+                if (!wait_warp(smem_u32(empty + st), ((it / NS) & 1) ^ 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const int nbox = __popc(__ballot_sync(0xffffffffu, mine));
+                const uint32_t bar = smem_u32(full + it % NB);
+                if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(2 * nbox * box * D * 2));
+                __syncwarp();
+                if (mine) {
+                    const int r = (pg * a.Hkv + hk) * a.page + tok % a.page;
+                    const uint32_t off = st * L::TILE + static_cast<uint32_t>(lane * box) * 128u;
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    tma_load_2d(sbase + L::K + off + h * 8192u, &tmK, h * 64, r, smem_u32(full + st));
-                    tma_load_2d(sbase + L::V + off + h * 8192u, &tmV, h * 64, r, smem_u32(full + st));
+                    for (int h = 0; h < D / 64; ++h) {
+                        tma_load_2d(sbase + L::K + off + h * 8192u, &tmK, h * 64, r, bar);
+                        tma_load_2d(sbase + L::V + off + h * 8192u, &tmV, h * 64, r, bar);
+                    }
                 }
             }
         }
         // no copy outlives the CTA
         if (lane == 0)
-            for (int st = 0; st < NS && st < it; ++st)
-                wait_bar_drain(smem_u32(full + st), (((it - 1 - st) / NS) & 1));
+            for (uint32_t k = 0; k < NB && k < it; ++k) wait_bar_drain(smem_u32(full + k), ((it - 1 - k) / NB) & 1);
         __syncwarp();
-    } else {
-        // =========================== arithmetic: 16 tokens of each tile
-        const int g = lane >> 2, tq = lane & 3;
+        return;
+    }
+
+    // =========================== arithmetic: 32 tokens of every second tile
+    const int g = lane >> 2, tq = lane & 3;
+    float* jo = reinterpret_cast<float*>(smem + L::JO);
+    float* jm = reinterpret_cast<float*>(smem + L::JM);
+    float* jl = jm + DEC_WARPS * 8;
+    uint32_t it = 0, joins = 0;
+    for (int seq = 0;; ++seq) {
+        const int slot = seq & 1;
+        if (!wait_warp(smem_u32(item_full + slot), (seq >> 1) & 1, abort_flag)) return;
+        const int b = items[slot * 4], hg = items[slot * 4 + 1], t0 = items[slot * 4 + 2], t1 = items[slot * 4 + 3];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(item_empty + slot));
+        if (t1 < 0) return;
+        const int hk = hg / a.gchunks, gc = hg - hk * a.gchunks;
+        const int head0 = hk * a.group + gc * 16;                 // first query head of the item
+        const int nheads = min(16, a.group - gc * 16);
+
+        float o[NT][D / 16][4];
+        float m[NT][2], l[NT][2];
         uint32_t qf[NT][D / 16][2];        // Q^T: head g of the tile, elements 2 tq .. of each 16
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][d][i] = 0.f;
             const int h = n * 8 + g;
             const __nv_bfloat16* qr = a.q + static_cast<long long>(b) * a.q_stride + static_cast<long long>(head0 + h) * D;
 #pragma unroll
@@ -316,158 +386,192 @@ __global__ void __launch_bounds__(DEC_THREADS, DEC_CTAS)
                 for (int i = 0; i < 2; ++i)
                     qf[n][kk][i] = h < nheads ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + i * 8 + 2 * tq)) : 0u;
         }
-        for (int it = 0; it < tiles; ++it) {
-            const int st = it % NS;
-            if (!wait_warp(smem_u32(full + st), (it / NS) & 1, abort_flag)) break;
-            const int left = t1 - (t0 + it * DEC_TILE + warp * 16);    // tokens of this warp's 16 that exist
+        const uint32_t tiles = static_cast<uint32_t>((t1 - t0 + DEC_TILE - 1) / DEC_TILE);
+        for (uint32_t i = (it ^ static_cast<uint32_t>(warp >> 1)) & 1u; i < tiles; i += 2) {
+            const uint32_t k = it + i;
+            const int st = k % NS;
+            if (!wait_warp(smem_u32(full + k % NB), (k / NB) & 1, abort_flag)) return;
+            const int left = t1 - (t0 + static_cast<int>(i) * DEC_TILE + (warp & 1) * 32);   // of 32 tokens that exist
             if (left > 0) {
                 const uint32_t kt = sbase + L::K + st * L::TILE, vt = sbase + L::V + st * L::TILE;
-                float s[NT][4];
+                float s[2][NT][4];        // two rows of 16 tokens
 #pragma unroll
-                for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+                for (int z = 0; z < 2; ++z)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) s[z][n][0] = s[z][n][1] = s[z][n][2] = s[z][n][3] = 0.f;
                 {
-                    const int r = warp * 16 + (lane & 15);
+                    const int r = (warp & 1) * 32 + (lane & 15);
                     const uint32_t rb = kt + static_cast<uint32_t>(r) * 128u;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        uint32_t af[4];
-                        ldsm_x4(af, rb + (kk >> 2) * 8192u + ((((kk & 3) * 2 + (lane >> 4)) ^ (r & 7)) * 16u));
+                    for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_16816(s[n], af, qf[n][kk][0], qf[n][kk][1]);
-                    }
+                        for (int z = 0; z < 2; ++z) {
+                            uint32_t af[4];
+                            ldsm_x4(af, rb + z * 2048u + (kk >> 2) * 8192u + ((((kk & 3) * 2 + (lane >> 4)) ^ (r & 7)) * 16u));
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma_16816(s[z][n], af, qf[n][kk][0], qf[n][kk][1]);
+                        }
                 }
-                // token g: s[.][0..1], token g + 8: s[.][2..3]; heads 2 tq, 2 tq + 1 of the tile
-                const bool v0 = g < left, v1 = g + 8 < left;
-                uint32_t pb[NT][2];
+                // row z, token g: s[z][.][0..1], token g + 8: s[z][.][2..3]; heads 2 tq, 2 tq + 1 of the tile
+                uint32_t pb[2][NT][2];
+                bool same = true;
+                float alpha[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float x0 = v0 ? s[n][i] * a.scale_log2 : -INFINITY;
-                        const float x1 = v1 ? s[n][2 + i] * a.scale_log2 : -INFINITY;
-                        float mx = fmaxf(x0, x1);
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            s[z][n][i] = z * 16 + g < left ? s[z][n][i] * a.scale_log2 : -INFINITY;
+                            s[z][n][2 + i] = z * 16 + g + 8 < left ? s[z][n][2 + i] * a.scale_log2 : -INFINITY;
+                            mx = fmax3(mx, s[z][n][i], s[z][n][2 + i]);
+                        }
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                         const float mn = fmaxf(m[n][i], mx);
                         const float ref = mn == -INFINITY ? 0.f : mn;      // scores of -inf only: P is 0
-                        const float alpha = ex2_approx(m[n][i] - ref);
-                        const float p0 = ex2_approx(x0 - ref), p1 = ex2_approx(x1 - ref);
-                        l[n][i] = l[n][i] * alpha + p0 + p1;
-                        m[n][i] = mn;
-                        s[n][i] = p0;
-                        s[n][2 + i] = p1;
+                        alpha[n][i] = ex2_approx(m[n][i] - ref);
+                        same = same && mn == m[n][i];
+                        float sum = 0.f;
 #pragma unroll
-                        for (int d = 0; d < D / 16; ++d) {
-                            o[n][d][i] *= alpha;
-                            o[n][d][2 + i] *= alpha;
+                        for (int z = 0; z < 2; ++z) {
+                            s[z][n][i] = ex2_approx(s[z][n][i] - ref);
+                            s[z][n][2 + i] = ex2_approx(s[z][n][2 + i] - ref);
+                            sum += s[z][n][i] + s[z][n][2 + i];
                         }
+                        l[n][i] = l[n][i] * alpha[n][i] + sum;
+                        m[n][i] = mn;
                     }
-                    pb[n][0] = movm_t(pack_bf16x2(s[n][0], s[n][1]));
-                    pb[n][1] = movm_t(pack_bf16x2(s[n][2], s[n][3]));
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        pb[z][n][0] = movm_t(pack_bf16x2(s[z][n][0], s[z][n][1]));
+                        pb[z][n][1] = movm_t(pack_bf16x2(s[z][n][2], s[z][n][3]));
+                    }
                 }
-                // values of tokens that do not exist are taken as 0 (0 times what is there could be NaN);
-                // lane words hold tokens 2 tq, 2 tq + 1 (words 0, 1) and 8 further (words 2, 3)
-                const uint32_t k0 = (2 * tq < left ? 0x0000FFFFu : 0u) | (2 * tq + 1 < left ? 0xFFFF0000u : 0u);
-                const uint32_t k1 = (2 * tq + 8 < left ? 0x0000FFFFu : 0u) | (2 * tq + 9 < left ? 0xFFFF0000u : 0u);
-                const int r = warp * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
-                const uint32_t rb = vt + static_cast<uint32_t>(r) * 128u;
+                if (!__all_sync(0xffffffffu, same)) {     // a maximum moved: O to the new one
 #pragma unroll
-                for (int d = 0; d < D / 16; ++d) {
-                    uint32_t af[4];
-                    ldsm_x4_t(af, rb + (d >> 2) * 8192u + ((((d & 3) * 2 + ((lane >> 3) & 1)) ^ (r & 7)) * 16u));
-                    if (left < 16) {
-                        af[0] &= k0;
-                        af[1] &= k0;
-                        af[2] &= k1;
-                        af[3] &= k1;
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[n][d][i] *= alpha[n][i & 1];
+                }
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const int lz = left - z * 16;
+                    // values of tokens that do not exist are taken as 0 (0 times what is there could be NaN);
+                    // lane words hold tokens 2 tq, 2 tq + 1 (words 0, 1) and 8 further (words 2, 3)
+                    const uint32_t k0 = (2 * tq < lz ? 0x0000FFFFu : 0u) | (2 * tq + 1 < lz ? 0xFFFF0000u : 0u);
+                    const uint32_t k1 = (2 * tq + 8 < lz ? 0x0000FFFFu : 0u) | (2 * tq + 9 < lz ? 0xFFFF0000u : 0u);
+                    const int r = (warp & 1) * 32 + z * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
+                    const uint32_t rb = vt + static_cast<uint32_t>(r) * 128u;
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d) {
+                        uint32_t af[4];
+                        ldsm_x4_t(af, rb + (d >> 2) * 8192u + ((((d & 3) * 2 + ((lane >> 3) & 1)) ^ (r & 7)) * 16u));
+                        if (lz < 16) {
+                            af[0] &= k0;
+                            af[1] &= k0;
+                            af[2] &= k1;
+                            af[3] &= k1;
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_16816(o[n][d], af, pb[z][n][0], pb[z][n][1]);
                     }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_16816(o[n][d], af, pb[n][0], pb[n][1]);
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(empty + st));
         }
-    }
+        it += tiles;
 
-    // ---- join the four warps through the ring's memory (every load has landed)
-    __syncthreads();
-    if (*abort_flag) return;
-    float* jm = reinterpret_cast<float*>(smem);                  // [warp][16] maximum
-    float* jl = jm + DEC_WARPS * 16;                             // [warp][16] sum
-    float* jo = jl + DEC_WARPS * 16;                             // [warp][head][D + 4]
-    constexpr int JP = D + 4;
-    static_assert((2 * DEC_WARPS * 16 + DEC_WARPS * 16 * JP) * 4 <= L::BARS, "join buffer");
-    if (warp < DEC_WARPS) {
-        const int g = lane >> 2, tq = lane & 3;
+        // ---- join the four warps, 8 heads and 64 elements at a time
+        const int part = t0 / a.tokens;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            if (n * 8 >= nheads) break;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float sum = l[n][i];
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const int h = n * 8 + 2 * tq + i;
-                if (g == 0) {
-                    jm[warp * 16 + h] = m[n][i];
-                    jl[warp * 16 + h] = sum;
+                for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], d);
+#pragma unroll
+            for (int e0 = 0; e0 < D; e0 += 64) {
+                if (joins > 0 && !wait_warp(smem_u32(join_free), (joins - 1) & 1, abort_flag)) return;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int h = 2 * tq + i;
+                    if (g == 0) {
+                        jm[warp * 8 + h] = m[n][i];
+                        jl[warp * 8 + h] = l[n][i];
+                    }
+                    // (element e of head h at e + 8 (h / 2), so that the four heads' lanes meet other banks)
+                    float* dst = jo + (warp * 8 + h) * 64;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        dst[(d * 16 + g + 8 * tq) & 63] = o[n][e0 / 16 + d][i];
+                        dst[(d * 16 + 8 + g + 8 * tq) & 63] = o[n][e0 / 16 + d][2 + i];
+                    }
                 }
-                float* dst = jo + (warp * 16 + h) * JP;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(join_full));
+                if (!wait_warp(smem_u32(join_full), joins & 1, abort_flag)) return;
+                const int count = min(8, nheads - n * 8) * 64;
+                for (int i = threadIdx.x; i < count; i += 32 * DEC_WARPS) {
+                    const int h = i >> 6, e = i & 63, d = e0 + e, at8 = (e + 8 * (h >> 1)) & 63;
+                    float mx = -INFINITY;
 #pragma unroll
-                for (int d = 0; d < D / 16; ++d) {
-                    dst[d * 16 + g] = o[n][d][i];
-                    dst[d * 16 + 8 + g] = o[n][d][2 + i];
+                    for (int w = 0; w < DEC_WARPS; ++w) mx = fmaxf(mx, jm[w * 8 + h]);
+                    const float ref = mx == -INFINITY ? 0.f : mx;
+                    float sum = 0.f, acc = 0.f;
+#pragma unroll
+                    for (int w = 0; w < DEC_WARPS; ++w) {
+                        const float f = ex2_approx(jm[w * 8 + h] - ref);
+                        sum += jl[w * 8 + h] * f;
+                        acc += jo[(w * 8 + h) * 64 + at8] * f;
+                    }
+                    const long long at = static_cast<long long>(b) * a.Hq + head0 + n * 8 + h;
+                    if (a.parts == 1) {
+                        a.o[at * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
+                        if (a.lse && d == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+                    } else {
+                        const long long pt = at * a.parts + part;
+                        a.part_o[pt * D + d] = acc;
+                        if (d == 0) a.part_ml[pt] = make_float2(mx, sum);
+                    }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(join_free));
+                ++joins;
             }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < nheads * D; i += DEC_THREADS) {
-        const int h = i / D, d = i - h * D;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < DEC_WARPS; ++w) mx = fmaxf(mx, jm[w * 16 + h]);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f, acc = 0.f;
-#pragma unroll
-        for (int w = 0; w < DEC_WARPS; ++w) {
-            const float f = ex2_approx(jm[w * 16 + h] - ref);
-            sum += jl[w * 16 + h] * f;
-            acc += jo[(w * 16 + h) * JP + d] * f;
-        }
-        const long long at = static_cast<long long>(b) * a.Hq + head0 + h;
-        if (a.parts == 1) {
-            a.o[at * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
-            if (a.lse && d == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
-        } else {
-            const long long pt = at * a.parts + part;
-            a.part_o[pt * D + d] = acc;
-            if (d == 0) a.part_ml[pt] = make_float2(mx, sum);
         }
     }
 }
 
-// One warp per (sequence, query head): join the parts that hold tokens.
-template <int D>
-__global__ void __launch_bounds__(128) cache_join_kernel(const DecArgs a, int heads) {
-    const int lane = threadIdx.x & 31;
-    const int at = blockIdx.x * 4 + (threadIdx.x >> 5);
+// One CTA of W warps per (sequence, query head): join the parts that hold
+// tokens.  Warp w takes parts w, w + W, .. in order, and the W are added in
+// order.  (A single head of 100000 tokens, 224 parts: 9 us with four warps.)
+template <int D, int W>
+__global__ void __launch_bounds__(32 * W) cache_join_kernel(const DecArgs a) {
+    constexpr int V = D / 32;          // elements a lane
+    __shared__ float s_o[W][D], s_l[W];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long at = blockIdx.x;
     pdl_wait();
-    if (at >= heads) return;
-    const int len = cache_len(a, at / a.Hq);
-    const int n = (len + a.tokens - 1) / a.tokens;
-    const float2* ml = a.part_ml + static_cast<long long>(at) * a.parts;
-    const float* po = a.part_o + static_cast<long long>(at) * a.parts * D;
+    const int len = cache_len(a, static_cast<int>(at / a.Hq));
+    const int n = static_cast<int>((static_cast<long long>(len) + a.tokens - 1) / a.tokens);
+    const float2* ml = a.part_ml + at * a.parts;
+    const float* po = a.part_o + at * a.parts * D;
     float mx = -INFINITY;
     for (int p = lane; p < n; p += 32) mx = fmaxf(mx, ml[p].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     const float ref = mx == -INFINITY ? 0.f : mx;
-    constexpr int V = D / 32;          // elements a lane
     float acc[V], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < n; ++p) {
+#pragma unroll 8
+    for (int p = warp; p < n; p += W) {
         const float2 x = ml[p];
         const float f = ex2_approx(x.x - ref);
         sum += x.y * f;
@@ -475,9 +579,21 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const DecArgs a, int he
         for (int i = 0; i < V; ++i) acc[i] += po[static_cast<long long>(p) * D + i * 32 + lane] * f;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        a.o[static_cast<long long>(at) * D + i * 32 + lane] = __float2bfloat16(sum == 0.f ? 0.f : acc[i] / sum);
-    if (a.lse && lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+    for (int i = 0; i < V; ++i) s_o[warp][i * 32 + lane] = acc[i];
+    if (lane == 0) s_l[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x < D) {
+        const int d = threadIdx.x;
+        float v = 0.f;
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            v += s_o[w][d];
+            sum += s_l[w];
+        }
+        a.o[at * D + d] = __float2bfloat16(sum == 0.f ? 0.f : v / sum);
+        if (a.lse && d == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -494,32 +610,31 @@ static bool cache_supported(int D, int page) {
 static bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// The split: as many parts as fill the GPU's CTA slots without a nearly empty
-// last round, at least 256 tokens a part.
+// The split: parts of one size, so many tokens that the items fill the GPU's
+// CTA slots once, but no more than 512 (1024 where over four query heads share
+// a key head, whose partial results weigh more): several items a slot even
+// out ragged lengths, and the ring runs on from one to the next.  At least
+// 128 tokens, and at most DEC_MAX_PARTS parts.
 static int split_parts(int B, int Hq, int Hkv, long long longest, int nsm, int* tokens) {
-    const int gchunks = (Hq / Hkv + 15) / 16;
-    const long long base = static_cast<long long>(B) * Hkv * gchunks;
+    const int group = Hq / Hkv;
+    const long long base = static_cast<long long>(B) * Hkv * ((group + 15) / 16);
     const long long slots = static_cast<long long>(nsm) * DEC_CTAS;
-    long long most = (longest + 255) / 256;
-    if (most < 1) most = 1;
-    if (most > DEC_MAX_PARTS) most = DEC_MAX_PARTS;
-    double best = 1e300;
-    auto time = [&](long long n) {
-        const double rounds = static_cast<double>((base * n + slots - 1) / slots);
-        const double chunk = static_cast<double>((longest + n - 1) / n);
-        return rounds * (chunk + 200.0);       // a CTA's fixed cost is that of about 200 tokens
-    };
-    for (long long n = 1; n <= most; ++n)
-        if (time(n) < best) best = time(n);
-    long long pick = 1;
-    for (long long n = 1; n <= most; ++n)
-        if (time(n) <= 1.05 * best) pick = n;
-    long long tk = (longest + pick - 1) / pick;
+    const long long most = group > 4 ? 1024 : 512;
+    const double once = static_cast<double>(longest) * static_cast<double>(base) / static_cast<double>(slots);
+    long long tk = once > static_cast<double>(most) ? most : static_cast<long long>(once);
+    if (tk < 128) tk = 128;
+    const long long least = (longest + DEC_MAX_PARTS - 1) / DEC_MAX_PARTS;
+    if (tk < least) tk = least;
     tk = (tk + DEC_TILE - 1) / DEC_TILE * DEC_TILE;
-    if (tk < DEC_TILE) tk = DEC_TILE;
     *tokens = static_cast<int>(tk);
     const long long parts = (longest + tk - 1) / tk;
     return parts < 1 ? 1 : static_cast<int>(parts);
+}
+
+static size_t attn_ws(int B, int Hq, int D, int parts) {
+    if (parts < 2) return 0;
+    const size_t n = static_cast<size_t>(B) * Hq * parts;
+    return (n * 8 + 255) / 256 * 256 + n * D * 4;
 }
 
 static int current_sms() {
@@ -530,26 +645,36 @@ static int current_sms() {
 }
 
 template <int D, int NT>
-static int launch_cache_attn(const CUtensorMap& tk, const CUtensorMap& tv, const DecArgs& a, int B, cudaStream_t s) {
+static int launch_cache_attn(const CUtensorMap& tk, const CUtensorMap& tv, const DecArgs& a, int B, int nsm,
+                             cudaStream_t s) {
     using L = DecSmem<D>;
-    if (cudaFuncSetAttribute(cache_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(L::TOTAL)) != cudaSuccess)
-        return FVATTN_ERR_CUDA;
-    const dim3 grid(static_cast<unsigned>(a.parts), static_cast<unsigned>(a.Hkv * a.gchunks), static_cast<unsigned>(B));
-    cache_attn_kernel<D, NT><<<grid, DEC_THREADS, L::TOTAL, s>>>(tk, tv, a);
+    static std::atomic<unsigned long long> ready{0};   // devices on which the kernel has its shared memory
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return FVATTN_ERR_CUDA;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if ((ready.load(std::memory_order_relaxed) & bit) == 0ull) {
+        if (cudaFuncSetAttribute(cache_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(L::TOTAL)) != cudaSuccess)
+            return FVATTN_ERR_CUDA;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    const long long items = static_cast<long long>(B) * a.Hkv * a.gchunks * a.parts;
+    const long long slots = static_cast<long long>(nsm) * DEC_CTAS;
+    cache_attn_kernel<D, NT><<<static_cast<unsigned>(items < slots ? items : slots), DEC_THREADS, L::TOTAL, s>>>(tk, tv, a);
     FV_CHECK_LAUNCH();
     if (a.parts == 1) return FVATTN_OK;
     cudaLaunchConfig_t cfg = {};
-    const int heads = B * a.Hq;
-    cfg.gridDim = dim3(static_cast<unsigned>((heads + 3) / 4));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(static_cast<unsigned>(B) * static_cast<unsigned>(a.Hq));
+    cfg.blockDim = dim3(a.parts > 32 ? 512 : 128);
     cfg.stream = s;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, a, heads) != cudaSuccess) return FVATTN_ERR_CUDA;
+    const cudaError_t e = a.parts > 32 ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, 16>, a)
+                                       : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, 4>, a);
+    if (e != cudaSuccess) return FVATTN_ERR_CUDA;
     return FVATTN_OK;
 }
 
@@ -638,9 +763,7 @@ extern "C" int fvattn_cache_attn_parts(int B, int Hq, int Hkv, int D, long long 
 
 extern "C" size_t fvattn_cache_attn_workspace_size(int B, int Hq, int Hkv, int D, long long longest) {
     const int parts = fvattn_cache_attn_parts(B, Hq, Hkv, D, longest, nullptr);
-    if (parts < 2) return 0;
-    const size_t n = static_cast<size_t>(B) * Hq * parts;
-    return (n * 8 + 255) / 256 * 256 + n * D * 4;
+    return attn_ws(B, Hq, D, parts);
 }
 
 extern "C" int fvattn_cache_attn(const fvattn_cache* c, int B, int Hq, const void* q, long long q_stride,
@@ -661,10 +784,12 @@ extern "C" int fvattn_cache_attn(const fvattn_cache* c, int B, int Hq, const voi
     a.gchunks = (a.group + 15) / 16;
     if (static_cast<long long>(a.Hkv) * a.gchunks > 65535 || static_cast<long long>(B) * Hq > 0x7fffffffll)
         return FVATTN_ERR_UNSUPPORTED;
-    a.parts = split_parts(B, Hq, c->Hkv, longest, current_sms(), &a.tokens);
+    const int nsm = current_sms();
+    a.B = B;
+    a.parts = split_parts(B, Hq, c->Hkv, longest, nsm, &a.tokens);
     if (a.parts > 1) {
-        const size_t need = fvattn_cache_attn_workspace_size(B, Hq, c->Hkv, c->D, longest);
-        if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < need)
+        if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+            ws_bytes < attn_ws(B, Hq, c->D, a.parts))
             return FVATTN_ERR_INVALID;
         const size_t n = static_cast<size_t>(B) * Hq * a.parts;
         a.part_ml = static_cast<float2*>(workspace);
@@ -691,8 +816,8 @@ extern "C" int fvattn_cache_attn(const fvattn_cache* c, int B, int Hq, const voi
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool two = a.group > 8;
     if (c->D == 128)
-        return two ? launch_cache_attn<128, 2>(tk, tv, a, B, s) : launch_cache_attn<128, 1>(tk, tv, a, B, s);
-    return two ? launch_cache_attn<64, 2>(tk, tv, a, B, s) : launch_cache_attn<64, 1>(tk, tv, a, B, s);
+        return two ? launch_cache_attn<128, 2>(tk, tv, a, B, nsm, s) : launch_cache_attn<128, 1>(tk, tv, a, B, nsm, s);
+    return two ? launch_cache_attn<64, 2>(tk, tv, a, B, nsm, s) : launch_cache_attn<64, 1>(tk, tv, a, B, nsm, s);
 }
 
 int fv::take_status_cache() { return fv::take_tu_status(); }
