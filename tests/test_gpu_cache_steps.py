@@ -1,0 +1,289 @@
+"""The cache operators as a generating program runs them: append and attend
+step by step, captured, on other streams, with shared pages, bad tables and
+long pools.  Bounds are those of test_gpu_cache."""
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_cache import BF16, I32, U, attend_definition, ca, check_attend, fv, pool, rotate  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def bits(t):
+    return t.view(torch.int16)
+
+
+def normal(shape, seed, scale=1.0):
+    return (torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda") * scale).to(BF16)
+
+
+@pytest.mark.parametrize("hq,hkv,D,page,axes,halves", [(6, 2, 64, 16, (32,), True), (4, 4, 128, 64, (22, 21, 21), False)])
+def test_generation(fv, ca, hq, hkv, D, page, axes, halves):  # noqa: F811
+    """A first part of each sequence appended at once, then token after token; at every step the attention is that of
+    the whole history, whose keys were rotated by their positions when they came."""
+    B, first, steps = 3, [5, page * 2, 1], page + 3
+    most = max(first) + steps
+    width = -(-most // page)
+    c = ca.PagedCache(*(torch.full((B * width, hkv, page, D), float("nan"), dtype=BF16, device="cuda") for _ in range(2)))
+    order = torch.randperm(B * width, generator=torch.Generator().manual_seed(1)).to(I32).view(B, width)
+    table = torch.full((B, width), -1, dtype=I32, device="cuda")       # pages are handed out as they are needed
+    rot = ca.rotation_table(D, axes, 512)
+    n_ax = len(axes)
+    ax = torch.repeat_interleave(torch.arange(n_ax), torch.tensor(axes)).cuda()
+    col = torch.arange(D // 2, device="cuda")
+    ks, vs = [[] for _ in range(B)], [[] for _ in range(B)]
+    lens = [0] * B
+    for step in range(steps):
+        new = first if step == 0 else [1] * B
+        rows = sum(new)
+        qkv = normal((rows, hq + 2 * hkv, D), 100 + step)
+        q, k, v = qkv[:, :hq], qkv[:, hq: hq + hkv], qkv[:, hq + hkv:]
+        pos = torch.randint(0, 512, (rows, n_ax), generator=torch.Generator().manual_seed(step), dtype=I32).cuda()
+        lens = [a + b for a, b in zip(lens, new)]
+        for b in range(B):
+            for p in range(-(-lens[b] // page)):
+                table[b, p] = order[b, p]
+        ln = torch.tensor(lens, dtype=I32, device="cuda")
+        cu = torch.tensor([0] + new).cumsum(0).to(I32).cuda() if step == 0 else None
+        qr = c.append(k, v, table, ln, cu=cu, q=q, pos=pos, rot=rot, axes=axes, halves=halves)
+        at = pos.long()[:, ax]
+        cos, sin = rot[at, col], rot[at, col + D // 2]
+        kr, kb = rotate(k, cos, sin, halves)
+        wq, qb = rotate(q, cos, sin, halves)
+        assert ((qr.double() - wq).abs() <= qb).all()
+        t, last = 0, []
+        for b in range(B):
+            for _ in range(new[b]):
+                ks[b].append(kr[t].to(BF16))
+                vs[b].append(v[t])
+                t += 1
+            last.append(t - 1)
+        qn = qr[last].contiguous()
+        o, lse = c.attend(qn, table, ln, longest=most)
+        want = attend_definition(c, qn, table, ln, 1 / math.sqrt(D))
+        check_attend((o, lse), want)
+        # and the cache holds the history: V as it came, K within a rounding of the rotated key
+        for b in range(B):
+            pages = table[b, : -(-lens[b] // page)].long()
+            hv = c.v_pages[pages].transpose(0, 1).reshape(hkv, -1, D)[:, : lens[b]]
+            assert torch.equal(hv, torch.stack(vs[b], 1))
+            hk = c.k_pages[pages].transpose(0, 1).reshape(hkv, -1, D)[:, : lens[b]].double()
+            wk = torch.stack(ks[b], 1).double()
+            # the kernel's rounding and the test's of the same sum: a step apart at most, plus the fp32 sum's error
+            assert ((hk - wk).abs() <= 2 * U * wk.abs() + 2.0 ** -20).all()
+    assert fv.get_status() == 0
+
+
+def test_captured_step_reads_the_current_tables(fv, ca):  # noqa: F811
+    hq, hkv, D, page, B = 8, 4, 128, 32, 4
+    lens = [700, 33, 1, 320]
+    c, table, ln = pool(ca, [x + 64 for x in lens], hkv, D, page, 3)
+    longest = 800
+    rot = ca.rotation_table(D, (64,), 1000)
+    q, k, v = normal((B, hq, D), 1), normal((B, hkv, D), 2), normal((B, hkv, D), 3)
+    qr, o, lse = torch.empty_like(q), torch.empty_like(q), torch.empty((B, hq), device="cuda")
+    pos = torch.zeros((B, 1), dtype=I32, device="cuda")
+    ws = c.attend_workspace(B, hq, longest)
+    ln.copy_(torch.tensor(lens, dtype=I32))
+
+    def step():
+        c.append(k, v, table, ln, q=q, q_out=qr, pos=pos, rot=rot)
+        c.attend(qr, table, ln, longest=longest, out=o, lse=lse, workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(1, 4):
+        now = [x + 17 * i for x in lens]
+        ln.copy_(torch.tensor(now, dtype=I32))
+        pos.copy_((ln - 1).view(B, 1))
+        for t, s in ((q, 10), (k, 20), (v, 30)):
+            t.copy_(normal(t.shape, s + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        kp, vp = c.k_pages.clone(), c.v_pages.clone()
+        want = attend_definition(c, qr, table, ln, 1 / math.sqrt(D))
+        check_attend((o, lse), want)
+        got = (o.clone(), lse.clone(), qr.clone())
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(c.k_pages), bits(kp)) and torch.equal(bits(c.v_pages), bits(vp))
+        assert torch.equal(bits(o), bits(got[0])) and torch.equal(lse, got[1]) and torch.equal(bits(qr), bits(got[2]))
+    assert fv.get_status() == 0
+
+
+@pytest.mark.parametrize("page,longest", [(16, 40), (64, 3000)])
+def test_many_sequences_some_empty(fv, ca, page, longest):  # noqa: F811
+    """More sequences than a warp has lanes, runs of empty ones, split and not split."""
+    B = 150
+    lens = [0 if 40 < b < 75 or b % 7 == 0 or b > 146 else (b * 7919) % (longest + 1) for b in range(B)]
+    lens[100] = longest
+    c, table, ln = pool(ca, lens, 2, 64, page, 5)
+    q = normal((B, 6, 64), 4, 2.0)
+    got = c.attend(q, table, ln, longest=longest)
+    assert fv.get_status() == 0
+    check_attend(got, attend_definition(c, q, table, ln, 0.125))
+    # a sequence's bits do not depend on the others: alone, with the same split
+    parts = ca.load().fvattn_cache_attn_parts
+    if parts(B, 6, 2, 64, longest, None) == parts(1, 6, 2, 64, longest, None) == 1:
+        one = c.attend(q[100:101], table[100:101].contiguous(), ln[100:101].contiguous(), longest=longest)
+        assert torch.equal(bits(one[0][0]), bits(got[0][100])) and torch.equal(one[1][0], got[1][100])
+
+
+def test_results_do_not_depend_on_the_schedule(fv, ca):  # noqa: F811
+    c, table, ln = pool(ca, [5000, 1, 2222, 700], 4, 128, 16, 5)
+    q = normal((4, 16, 128), 4, 2.0)
+    first = c.attend(q, table, ln, longest=5000)
+    # lengths of the others change, the split (a host number) does not
+    ln2 = ln.clone()
+    ln2[1:] = torch.tensor([3, 1000, 0], dtype=I32)
+    table2 = table.clone()
+    table2[1] = table[0]
+    second = c.attend(q, table2, ln2, longest=5000)
+    for a, b in zip(first, second):
+        assert torch.equal(a[0], b[0])
+    for _ in range(5):
+        again = c.attend(q, table, ln, longest=5000)
+        assert torch.equal(bits(again[0]), bits(first[0])) and torch.equal(again[1], first[1])
+
+
+def test_rows_past_the_end_may_hold_anything_and_scores_of_minus_infinity(fv, ca):  # noqa: F811
+    lens = [1, 17, 64, 100, 130]
+    c, table, ln = pool(ca, lens, 1, 64, 32, 7)
+    q = normal((5, 1, 64), 8).abs() + 0.5
+    want = attend_definition(c, q, table, ln, 0.125)
+    for b, n in enumerate(lens):
+        for p in range(-(-n // 32)):
+            used = min(32, n - 32 * p)
+            c.k_pages[table[b, p], :, used:] = float("nan")
+            c.v_pages[table[b, p], :, used:] = float("inf")
+    check_attend(c.attend(q, table, ln), want)
+    # keys of -inf: their scores are -inf and their values take no part; a sequence of such keys only is like an empty one
+    c.k_pages[table[0, 0], :, 0] = -float("inf")
+    c.k_pages[table[3, 1], :, 3:9] = -float("inf")
+    o, lse = c.attend(q, table, ln)
+    keep = torch.ones(100, dtype=torch.bool)
+    keep[35:41] = False
+    k = c.k_pages[table[3, :4].long()].transpose(0, 1).reshape(-1, 64)[:100][keep].double()
+    v = c.v_pages[table[3, :4].long()].transpose(0, 1).reshape(-1, 64)[:100][keep].double()
+    p = torch.softmax(q[3].double() @ k.T * 0.125, -1)
+    assert ((o[3].double() - p @ v).abs() <= 1.25 * U * (p @ v.abs() + (p @ v).abs())).all()
+    assert (o[0] == 0).all() and lse[0, 0] == -math.inf
+    assert fv.get_status() == 0
+
+
+def test_bad_pages_and_lengths_are_reported(fv, ca):  # noqa: F811
+    lens = [40, 50, 60]
+    c, table, ln = pool(ca, lens, 2, 64, 16, 9)
+    q, k, v = normal((3, 4, 64), 1), normal((3, 2, 64), 2), normal((3, 2, 64), 3)
+    want = c.attend(q, table, ln, longest=64)
+    k0 = c.k_pages.clone()
+    for bad in (-1, c.pages, 1 << 30):
+        t2 = table.clone()
+        t2[1, 1] = bad
+        got = c.attend(q, t2, ln, longest=64)
+        assert fv.get_status() == fv.ERR_BOUNDS
+        for b in (0, 2):
+            assert torch.equal(got[0][b], want[0][b]) and torch.equal(got[1][b], want[1][b])
+    t2 = table.clone()
+    t2[1, 3] = -7                       # page of sequence 1's token 49
+    c.append(k, v, t2, ln)
+    assert fv.get_status() == fv.ERR_BOUNDS
+    changed = (bits(c.k_pages) != bits(k0)).any(-1).any(1).nonzero()
+    assert {(int(p), int(r)) for p, r in changed} == {(int(table[0, 2]), 7), (int(table[2, 3]), 11)}
+    ln2 = ln.clone()
+    ln2[1] = 65
+    got = c.attend(q, table, ln2, longest=64)      # clamped to 64: of its 4 pages
+    assert fv.get_status() == fv.ERR_BOUNDS
+    assert torch.equal(got[0][0], c.attend(q, table, ln, longest=64)[0][0])
+    ln2[1] = -1
+    got = c.attend(q, table, ln2, longest=64)
+    assert fv.get_status() == fv.ERR_BOUNDS
+    assert (got[0][1] == 0).all() and (got[1][1] == -math.inf).all()
+    # a position outside the rotation table: that token is not written, nor its query
+    rot = ca.rotation_table(64, (32,), 100)
+    pos = torch.tensor([[5], [100], [-1]], dtype=I32, device="cuda")
+    k0, out = c.k_pages.clone(), torch.full_like(q, 3.0)
+    c.append(k, v, table, ln, q=q, q_out=out, pos=pos, rot=rot)
+    assert fv.get_status() == fv.ERR_BOUNDS
+    changed = (bits(c.k_pages) != bits(k0)).any(-1).any(1).nonzero()
+    assert {(int(p), int(r)) for p, r in changed} <= {(int(table[0, 2]), 7)}
+    assert (out[1:] == 3.0).all() and not (out[0] == 3.0).all()
+    assert fv.get_status() == 0
+
+
+def test_shared_pages_strided_queries_and_another_stream(fv, ca):  # noqa: F811
+    c, table, ln = pool(ca, [96, 96, 40], 2, 128, 32, 11)
+    table[1, :2] = table[0, :2]                    # a common prefix of 64 tokens
+    qkv = normal((3, 8 + 4, 128), 1)
+    q = qkv[:, :8]
+    want = attend_definition(c, q, table, ln, 1 / math.sqrt(128))
+    check_attend(c.attend(q, table, ln), want)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = c.attend(q, table, ln, stream=st)
+    torch.cuda.synchronize()
+    check_attend(got, want)
+    # in place: the rotated queries over the queries
+    rot = ca.rotation_table(128, (30, 34), 50)
+    pos = torch.randint(0, 50, (3, 2), dtype=I32, device="cuda")
+    kw = dict(pos=pos, rot=rot, axes=(30, 34))
+    out = c.append(qkv[:, 8:10], qkv[:, 10:], table, ln, q=q, **kw)
+    same = c.append(qkv[:, 8:10], qkv[:, 10:], table, ln, q=q, q_out=q, **kw)
+    assert same.data_ptr() == qkv.data_ptr() and torch.equal(bits(q.contiguous()), bits(out))
+    assert fv.get_status() == 0
+
+
+def test_nothing_to_append(fv, ca):  # noqa: F811
+    c, table, ln = pool(ca, [10, 20], 2, 64, 16, 11)
+    k0 = c.k_pages.clone()
+    empty = torch.empty((0, 2, 64), dtype=BF16, device="cuda")
+    zero = torch.zeros(3, dtype=I32, device="cuda")
+    assert c.append(empty, empty, table, ln, cu=zero) is None
+    k = normal((4, 2, 64), 1)
+    c.append(k, k, table, ln, cu=zero)             # four rows, all behind the last sequence
+    assert fv.get_status() == 0 and torch.equal(bits(c.k_pages), bits(k0))
+
+
+def test_pool_past_two_gigaelements(fv, ca):  # noqa: F811
+    """Pages whose elements lie past 2^31 (a pool of 4.3 GB a tensor)."""
+    D, hkv, page = 128, 8, 128
+    pages = (1 << 31) // (D * hkv * page) + 40
+    c = ca.PagedCache.empty(pages, hkv, D, page)
+    n, top = 700, 6
+    table = torch.arange(pages - top, pages, dtype=I32, device="cuda").flip(0).view(1, top).contiguous()
+    ln = torch.tensor([n], dtype=I32, device="cuda")
+    k, v = normal((n, hkv, D), 1), normal((n, hkv, D), 2)
+    c.append(k, v, table, ln, cu=torch.tensor([0, n], dtype=I32, device="cuda"))
+    q = normal((1, 16, D), 3, 2.0)
+    got = c.attend(q, table, ln)
+    assert fv.get_status() == 0
+    hk = c.k_pages[table[0].long()].transpose(0, 1).reshape(hkv, -1, D)[:, :n]
+    assert torch.equal(hk, k.transpose(0, 1))
+    check_attend(got, attend_definition(c, q, table, ln, 1 / math.sqrt(D)))
+
+
+def test_cache_refusals_on_the_gpu(fv, ca):  # noqa: F811
+    c, table, ln = pool(ca, [10, 20], 2, 64, 16, 11)
+    k, q = normal((2, 2, 64), 1), normal((2, 4, 64), 1)
+    for kw, match in ((dict(k=k.float()), "k:"), (dict(v=k[:, :1]), "v:"), (dict(k=k.transpose(0, 1).contiguous().transpose(0, 1)), "k:"),
+                      (dict(table=table.long()), "table"), (dict(lens=ln[:1]), "lens"), (dict(cu=ln), "cu"), (dict(q_out=q), "q_out"),
+                      (dict(pos=ln.view(2, 1)), "rot"), (dict(rot=torch.zeros((4, 32), device="cuda")), "rot"),
+                      (dict(rot=torch.zeros((4, 64), device="cuda")), "pos"),
+                      (dict(rot=torch.zeros((4, 64), device="cuda"), axes=(3, 4)), "axes")):
+        with pytest.raises(ValueError, match=match):
+            c.append(**{**dict(k=k, v=k, table=table, lens=ln), **kw})
+    for kw, match in ((dict(q=q[:, :3]), "divide"), (dict(q=q[:1]), "q:"), (dict(scale=0.0), "scale"), (dict(longest=-1), "longest"),
+                      (dict(out=q.float()), "out"), (dict(lse=q), "lse"), (dict(table=None), "table"),
+                      (dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"), longest=5000), "workspace")):
+        with pytest.raises(ValueError, match=match):
+            c.attend(**{**dict(q=q, table=table, lens=ln), **kw})
+    with pytest.raises(ValueError, match="distinct"):
+        ca.PagedCache(c.k_pages, c.k_pages)
+    with pytest.raises(ValueError, match="unsupported"):
+        ca.PagedCache(*(torch.zeros((2, 2, 24, 64), dtype=BF16, device="cuda") for _ in range(2)))
+    assert fv.get_status() == 0

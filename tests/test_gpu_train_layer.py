@@ -1,0 +1,329 @@
+"""Training through the layer, and the calls around the gradient operators that
+a training program makes: streams, graphs, several calls at once, bad lists,
+concentrated rows.  Bounds are those of test_gpu_train (u = 2^-8, half a bf16
+step); what is compared with another run of the same kernels has to have the
+same bits."""
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_train import SLACK, U, check, definition, fv, random_lists, tiles, tr  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+GEO = (1, 2, 128, 3, 19, 21, 2, 8, 8)
+GEO64 = (2, 2, 64, 3, 13, 21, 1, 8, 8)
+
+
+def raster(g, seed, n=4, scale=1.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return [(torch.randn((g.B, g.N, g.H, g.D), generator=gen, device="cuda") * (scale if i == 0 else 1.0)).to(BF16)
+            for i in range(n)]
+
+
+def bits(t):
+    return t.view(torch.int16)
+
+
+def dense(q, k, v, do, scale):
+    """O and gradients of dense attention on raster tensors in 64 bits, and test_gpu_train's bounds."""
+    q, k, v, do = (t.double().transpose(1, 2) for t in (q, k, v, do))
+    t = lambda m: m.transpose(-1, -2)  # noqa: E731
+    p = torch.softmax(q @ t(k) * scale, -1)
+    o = p @ v
+    ds = p * (do @ t(v) - (do * o).sum(-1, keepdim=True))
+    out = dict(o=o, dq=ds @ k * scale, dk=t(ds) @ q * scale, dv=t(p) @ do)
+    e = U * ds.abs() + p * U * (do.abs() * o.abs()).sum(-1, keepdim=True)
+    err = dict(o=U * (p @ v.abs()), dq=scale * (e @ k.abs()), dk=scale * (t(e) @ q.abs()), dv=U * (t(p) @ do.abs()))
+    return ({n: x.transpose(1, 2) for n, x in out.items()},
+            {n: (SLACK * (x + U * out[n].abs()) + 1e-30).transpose(1, 2) for n, x in err.items()})
+
+
+@pytest.mark.parametrize("order", ["raster", "hilbert"])
+@pytest.mark.parametrize("geo", [GEO, GEO64], ids=["bs128", "bs64"])
+def test_layer_that_keeps_every_block_is_dense_attention(fv, tr, geo, order):  # noqa: F811
+    g = fv.geom(*geo)
+    q, k, v, do = raster(g, 1, scale=1.5)
+    q, k, v = (t.requires_grad_() for t in (q, k, v))
+    layer = tr.TrainLayer(g, 1.0, 1, order=order)
+    o = layer(q, k, v)
+    o.backward(do)
+    assert fv.get_status() == 0
+    want, bound = dense(q.detach(), k.detach(), v.detach(), do, 1 / math.sqrt(g.D))
+    for name, got in (("o", o.detach()), ("dq", q.grad), ("dk", k.grad), ("dv", v.grad)):
+        check(got, want[name], bound[name], name)
+
+
+def test_gradients_agree_with_differences(fv, tr):  # noqa: F811
+    """The kernel's gradients along random directions against central differences of the loss sum(O * dO) in 64 bits
+    on the same lists.  Bound: the elements' bounds weighted with |direction|; the differences' own error is
+    h^2 / 6 of a third derivative, with h = 1e-4 below 1e-6 of the terms' sizes."""
+    g = fv.geom(*GEO64)
+    idx, cnt = random_lists(g, 0.5, 3, (1,))
+    q, k, v, do = tiles(g, 4, (1.5, 1.0, 1.0, 1.0))
+    scale = 1 / math.sqrt(g.D)
+    o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+    grads = tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt)
+    _, bound = definition(g, q, k, v, do, idx, cnt, scale)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    h = 1e-4
+    for i, name in enumerate(("dq", "dk", "dv")):
+        x = [q.double(), k.double(), v.double()]
+        real = (x[i].abs().sum(-1, keepdim=True) > 0)
+        d = torch.randn(q.shape, generator=gen, device="cuda", dtype=torch.float64) * real
+
+        def loss(s):
+            y = list(x)
+            y[i] = y[i] + s * h * d
+            return (definition(g, *y, do, idx, cnt, scale)[0]["o"] * do.double()).sum().item()
+
+        diff = (loss(1) - loss(-1)) / (2 * h)
+        got = (grads[i].double() * d).sum().item()
+        tol = (bound[name] * d.abs()).sum().item()
+        assert abs(got - diff) <= tol + 1e-5 * abs(diff), name
+
+
+def test_attention_function_is_the_operators_between_reorders(fv, tr):  # noqa: F811
+    g = fv.geom(*GEO)
+    idx, cnt = random_lists(g, 0.5, 6)
+    q, k, v, do = raster(g, 7)
+    q, k, v = (t.requires_grad_() for t in (q, k, v))
+    o = tr.attention(g, q, k, v, idx, cnt)
+    got = torch.autograd.grad(o, (q, k, v), do)
+    qt, kt, vt, dot = (fv.reorder(g, t.detach()) for t in (q, k, v, do))
+    ot, lse = tr.sparse_attn_lse(g, qt, kt, vt, idx, cnt)
+    assert torch.equal(bits(fv.inverse_reorder(g, ot)), bits(o.detach()))
+    for a, b in zip(got, tr.sparse_attn_bwd(g, qt, kt, vt, ot, dot, lse, idx, cnt)):
+        assert torch.equal(bits(a), bits(fv.inverse_reorder(g, b)))
+    # the forward's bits are those of the inference call
+    assert torch.equal(bits(ot), bits(fv.sparse_attn(g, qt, kt, vt, idx, cnt)))
+    # a gradient that is not contiguous, and one input that needs none
+    o = tr.attention(g, q, k.detach(), v, idx, cnt)
+    wide = torch.zeros((g.B, g.N, g.H, 2 * g.D), dtype=BF16, device="cuda")
+    wide[..., ::2] = do
+    dq, dv = torch.autograd.grad(o, (q, v), wide[..., ::2])
+    assert torch.equal(bits(dq), bits(got[0])) and torch.equal(bits(dv), bits(got[2]))
+
+
+def test_concentrated_rows_lose_no_precision(fv, tr):  # noqa: F811
+    """Scores of standard deviation 4: a row's softmax sits on a few keys, where dO . O from the rounded O would add
+    an error as large as the rounding of the result.  r0 is that rounding's relative 2-norm (of the 64-bit result
+    rounded to bf16); dS, rounded before its product, adds as much, independently, and tiles that keep to the rounded
+    O at most a quarter: sqrt(2 + 1/16) r0, with 5% for chance."""
+    g = fv.geom(1, 2, 64, 4, 16, 24, 2, 8, 8)
+    idx, cnt = random_lists(g, 0.8, 2)
+    q, k, v, do = tiles(g, 3, (4.0, 1.0, 1.0, 1.0))
+    o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+    got = tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt)
+    want, bound = definition(g, q, k, v, do, idx, cnt, 1 / math.sqrt(g.D))
+    for x, name in zip(got, ("dq", "dk", "dv")):
+        check(x, want[name], bound[name], name)
+        far = lambda y: ((y.double() - want[name]).norm() / want[name].norm()).item()  # noqa: B023, E731
+        assert far(x) <= 1.05 * math.sqrt(2 + 1 / 16) * far(want[name].to(BF16)), name
+
+
+def test_very_negative_scores(fv, tr):  # noqa: F811
+    """Every score of some rows near -300: exp2(-lse) of the padding keys, which are zeros, would overflow if it were
+    not masked there."""
+    g = fv.geom(*GEO)
+    idx, cnt = random_lists(g, 1.0, 2)
+    q, k, v, do = tiles(g, 3)
+    real = (k.abs().sum(-1, keepdim=True) > 0)
+    k = (torch.ones_like(k) * 2 + 0.1 * k.float()).to(BF16) * real
+    q = torch.where(torch.arange(g.Npad, device="cuda")[:, None] % 3 == 0, -13.0 - 0.0 * q, 0.3 * q).to(BF16)
+    q = q * (real if g.order is None else 1)
+    o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+    got = tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt)
+    assert fv.get_status() == 0
+    want, bound = definition(g, q, k, v, do, idx, cnt, 1 / math.sqrt(g.D))
+    assert want["lse"][~want["lse"].isinf()].min() < -250
+    # lse rounded to fp32 is off by 2^-24 * 300, which P = exp(s - lse) takes as a relative error of 2e-5 (and the
+    # products of that size add as much again): far below u, with 1% on the bounds
+    for x, name in zip(got, ("dq", "dk", "dv")):
+        check(x, want[name], 1.01 * bound[name], name)
+
+
+def test_two_streams_at_once_and_another_stream(fv, tr):  # noqa: F811
+    g = fv.geom(*GEO)
+    sets = []
+    for s in range(2):
+        idx, cnt = random_lists(g, 0.6, 20 + s)
+        q, k, v, do = tiles(g, 30 + s)
+        o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+        sets.append((q, k, v, o, do, lse, idx, cnt))
+    want = [tr.sparse_attn_bwd(g, *s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = []
+    for _ in range(3):
+        got = [tr.sparse_attn_bwd(g, *s, stream=st) for s, st in zip(sets, streams)]
+    torch.cuda.synchronize()
+    assert fv.get_status() == 0
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(bits(x), bits(y))
+
+
+def test_captured_operators_replay_on_new_inputs(fv, tr):  # noqa: F811
+    g = fv.geom(*GEO64)
+    idx, cnt = random_lists(g, 0.5, 1)
+    ins = tiles(g, 2)
+    q, k, v, do = (t.clone() for t in ins)
+    aw, bw = fv.attn_workspace(g), tr.bwd_workspace(g)
+    outs = [torch.empty_like(q) for _ in range(3)]
+    o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt, workspace=aw)
+    tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt, dq=outs[0], dk=outs[1], dv=outs[2], workspace=bw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tr.sparse_attn_lse(g, q, k, v, idx, cnt, out=o, lse=lse, workspace=aw)
+        tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt, dq=outs[0], dk=outs[1], dv=outs[2], workspace=bw)
+    for seed in (5, 6):
+        new = tiles(g, seed, (2.0, 1.0, 1.0, 1.0))
+        nidx, ncnt = random_lists(g, 0.7, seed, (2,))
+        for t, n in zip((q, k, v, do, idx, cnt), (*new, nidx, ncnt)):
+            t.copy_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        wo, wl = tr.sparse_attn_lse(g, *new[:3], nidx, ncnt)
+        want = tr.sparse_attn_bwd(g, *new[:3], wo, new[3], wl, nidx, ncnt)
+        for a, b in zip(outs, want):
+            assert torch.equal(bits(a), bits(b))
+    assert fv.get_status() == 0
+
+
+def test_captured_training_step(fv, tr):  # noqa: F811
+    """A whole step, routing to gradients, captured: autograd.grad on leaves that no eager graph uses."""
+    g = fv.geom(*GEO)
+    layer = tr.TrainLayer(g, 0.9, 2)
+    buf = [t for t in raster(g, 3)]
+    leaves = [t.detach().requires_grad_() for t in buf[:3]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(layer(*leaves), leaves, buf[3])
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = layer(*leaves)
+        got = torch.autograd.grad(o, leaves, buf[3])
+    new = raster(g, 8, scale=2.0)
+    with torch.no_grad():
+        for t, n in zip(leaves + [buf[3]], new):
+            t.copy_(n)
+    graph.replay()
+    torch.cuda.synchronize()
+    fresh = [t.clone().requires_grad_() for t in new[:3]]
+    wo = layer(*fresh)
+    want = torch.autograd.grad(wo, fresh, new[3])
+    assert torch.equal(bits(o.detach()), bits(wo.detach()))
+    for a, b in zip(got, want):
+        assert torch.equal(bits(a), bits(b))
+    assert fv.get_status() == 0
+
+
+def test_several_forwards_before_their_backwards(fv, tr):  # noqa: F811
+    g = fv.geom(*GEO64)
+    layer = tr.TrainLayer(g, 0.8, 2)
+    sets = [raster(g, s) for s in (1, 2)]
+    single = []
+    for q, k, v, do in sets:
+        x = [t.clone().requires_grad_() for t in (q, k, v)]
+        single.append(torch.autograd.grad(layer(*x), x, do))
+    xs = [[t.clone().requires_grad_() for t in s[:3]] for s in sets]
+    os_ = [layer(*x) for x in xs]
+    for x, o, s, want in reversed(list(zip(xs, os_, sets, single))):
+        for a, b in zip(torch.autograd.grad(o, x, s[3]), want):
+            assert torch.equal(bits(a), bits(b))
+    # the same tensor as q, k and v: its gradient is the sum of the three
+    x = sets[0][0].clone().requires_grad_()
+    do = sets[0][3]
+    (gx,) = torch.autograd.grad(layer(x, x, x), x, do)
+    parts = [sets[0][0].clone().requires_grad_() for _ in range(3)]
+    gp = torch.autograd.grad(layer(*parts), parts, do)
+    # autograd adds two bf16 sums, each rounded: 2 u of the terms' sizes
+    total = sum(t.double() for t in gp)
+    assert ((gx.double() - total).abs() <= 2 * U * sum(t.double().abs() for t in gp) + 1e-30).all()
+
+
+@pytest.mark.parametrize("what", ["count", "index", "twice"])
+def test_bad_lists_are_reported(fv, tr, what):  # noqa: F811
+    """Status word set; the bad entry is clamped, skipped or taken once; rows of other lists keep their results."""
+    g = fv.geom(*GEO64)
+    idx, cnt = random_lists(g, 0.6, 4)
+    q, k, v, do = tiles(g, 5)
+    o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+    want = tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt)
+    assert fv.get_status() == 0
+    bad_i, bad_c = idx.clone(), cnt.clone()
+    n = int(cnt[0, 0, 1])
+    if what == "count":
+        bad_c[0, 0, 1] = -3
+    elif what == "index":
+        bad_i[0, 0, 1, n - 1] = g.nb
+    else:
+        bad_c[0, 0, 1] = n + 1
+        bad_i[0, 0, 1, n] = bad_i[0, 0, 1, 0]
+    got = tr.sparse_attn_bwd(g, q, k, v, o, do, lse, bad_i, bad_c)
+    assert fv.get_status() == fv.ERR_BOUNDS
+    for a, b in zip(got, want):
+        assert torch.equal(bits(a[:, 1:]), bits(b[:, 1:]))       # the other heads
+    if what == "twice":
+        for a, b in zip(got, want):
+            assert torch.equal(bits(a), bits(b))
+    if what == "count":
+        assert (got[0][0, 0, g.bs: 2 * g.bs] == 0).all()
+
+
+def test_blocks_that_nobody_keeps_may_hold_anything(fv, tr):  # noqa: F811
+    """NaN and infinities in K and V blocks outside every list (128-token blocks): nothing of them is read."""
+    g = fv.geom(1, 1, 128, 2, 16, 32, 2, 8, 8)
+    idx, cnt = random_lists(g, 1.0, 1)
+    keep = [0, 2, 3, 5, 7]
+    cnt.fill_(len(keep))
+    idx[..., : len(keep)] = torch.tensor(keep, dtype=torch.int32, device="cuda")
+    q, k, v, do = tiles(g, 2)
+    o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+    want = tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt)
+    for j, x in ((1, float("nan")), (4, float("inf")), (6, -float("inf"))):
+        k[:, :, j * g.bs: (j + 1) * g.bs] = x
+        v[:, :, j * g.bs: (j + 1) * g.bs] = x
+    o2, lse2 = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+    assert torch.equal(bits(o), bits(o2)) and torch.equal(lse, lse2)
+    got = tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt)
+    # dK and dV of the blocks that nobody keeps are zero before and after; dQ reads kept blocks only.  (The choice of
+    # the tiles that sum delta again goes by the mean of |V|^2, which is not finite now: the two dQ agree within
+    # their bounds, not in their bits.)
+    clean = [torch.where(t.isfinite(), t, torch.zeros_like(t)) for t in (k, v)]
+    _, bound = definition(g, q, clean[0], clean[1], do, idx, cnt, 1 / math.sqrt(g.D))
+    for a, b, name in zip(got, want, ("dq", "dk", "dv")):
+        check(a, b.double(), 2 * bound[name], name)
+
+
+def test_refusals_on_the_gpu(fv, tr):  # noqa: F811
+    g = fv.geom(*GEO)
+    idx, cnt = random_lists(g, 0.5, 6)
+    q, k, v, do = tiles(g, 7)
+    o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+    ok = dict(qt=q, kt=k, vt=v, ot=o, dot=do, lse=lse, kv_idx=idx, kv_cnt=cnt)
+    for name, bad in (("qt", q[:, :1]), ("kt", k.float()), ("vt", v.transpose(2, 3)), ("ot", None), ("dot", do.cpu()),
+                      ("lse", lse.double()), ("kv_idx", idx.long()), ("kv_cnt", cnt[..., :-1])):
+        with pytest.raises(ValueError, match=name):
+            tr.sparse_attn_bwd(g, **{**ok, name: bad})
+    with pytest.raises(ValueError, match="distinct"):
+        tr.sparse_attn_bwd(g, **ok, dq=q)
+    with pytest.raises(ValueError, match="workspace"):
+        tr.sparse_attn_bwd(g, **ok, workspace=torch.empty(512, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="workspace"):
+        tr.sparse_attn_lse(g, q, k, v, idx, cnt, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="scale"):
+        tr.sparse_attn_lse(g, q, k, v, idx, cnt, scale=-1.0)
+    with pytest.raises(ValueError, match="input"):
+        tr.sparse_attn_lse(g, q, k, v, idx, cnt, out=v)
+    with pytest.raises(ValueError, match="order"):
+        tr.attention(fv.with_order(g, fv.block_order(g)), *(torch.zeros((g.B, g.N, g.H, g.D), dtype=BF16, device="cuda"),) * 3,
+                     idx, cnt)
+    assert fv.get_status() == 0
