@@ -863,29 +863,16 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, 
     for (int i = lane; i < nwords; i += 32) bits[unit * nwords + i] = mine[i];
 }
 
-// One warp per (direction, b, h, tile): the blocks that a tile of G blocks is
-// paired with, ascending, each with its membership bits above bit 24 (bit t:
-// paired with the tile's block t).  Direction 0: a query tile and key blocks,
-// from the rows of the bit matrix; 1: a key tile and query blocks, from its
-// columns.
-__global__ void __launch_bounds__(256) grad_lists_kernel(Geo g, int G, int ngroups, int nwords,
-                                                         const uint32_t* __restrict__ bits,
-                                                         uint32_t* __restrict__ ulq, int32_t* __restrict__ cntq,
-                                                         uint32_t* __restrict__ ulk, int32_t* __restrict__ cntk) {
+// The blocks that a tile of G blocks is paired with, ascending, each with its
+// membership bits above bit 24 (bit t: paired with the tile's block t); the
+// list's length.  Direction 0: a query tile u and key blocks, from the rows of
+// the bit matrix; 1 (keys): a key tile and query blocks, from its columns.
+// One warp.
+__device__ __forceinline__ int grad_list(const Geo& g, int G, int nwords, const uint32_t* __restrict__ mat, bool keys,
+                                         int u, uint32_t* __restrict__ dst) {
     const int lane = threadIdx.x & 31;
-    pdl_launch_dependents();
-    pdl_wait();
-    const long long units = static_cast<long long>(g.B) * g.H * ngroups;
-    long long unit = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const bool keys = unit >= units;
-    if (keys) unit -= units;
-    if (unit >= units) return;
-    const long long bh = unit / ngroups;
-    const int u = static_cast<int>(unit - bh * ngroups);
-    const uint32_t* mat = bits + bh * g.nb * nwords;
     int base = 0;
     if (!keys) {
-        uint32_t* dst = ulq + unit * g.nb;
         const int q0 = u * G, nq = min(G, g.nb - q0);
         for (int w0 = 0; w0 < nwords; w0 += 32) {
             const int wd = w0 + lane;
@@ -912,9 +899,7 @@ __global__ void __launch_bounds__(256) grad_lists_kernel(Geo g, int G, int ngrou
             }
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
-        if (lane == 0) cntq[unit] = base;
     } else {
-        uint32_t* dst = ulk + unit * g.nb;
         const int wd = (u * G) >> 5, sh = (u * G) & 31;   // G divides 32: one word holds the tile's columns
         const uint32_t ones = (1u << G) - 1u;
         for (int i0 = 0; i0 < g.nb; i0 += 32) {
@@ -924,36 +909,50 @@ __global__ void __launch_bounds__(256) grad_lists_kernel(Geo g, int G, int ngrou
             if (mem) dst[base + __popc(any & ((1u << lane) - 1u))] = static_cast<uint32_t>(i) | (mem << 24);
             base += __popc(any);
         }
-        if (lane == 0) cntk[unit] = base;
     }
+    return base;
 }
 
-// One CTA per (direction, b, h): the head's tiles by list length, longest
-// first (a counting sort; which of two equal tiles comes first changes only
-// the schedule), query tiles that need the exact delta with GRAD_FLAG.  The
-// first CTA of a direction resets its item counter.
-__global__ void __launch_bounds__(256) grad_order_kernel(Geo g, int G, int ngroups, const float2* __restrict__ norms,
-                                                         const int32_t* __restrict__ cntq,
-                                                         const int32_t* __restrict__ cntk, int32_t* __restrict__ ordq,
-                                                         int32_t* __restrict__ ordk, int* __restrict__ counters) {
+// One CTA per (direction, b, h): the lists of the head's tiles, and the tiles
+// by list length, longest first (a counting sort; which of two equal tiles
+// comes first changes only the schedule), query tiles that need the exact
+// delta with GRAD_FLAG.  The first CTA of a direction resets its item counter.
+constexpr int LISTS_THREADS = 1024;
+
+__global__ void __launch_bounds__(LISTS_THREADS) grad_lists_kernel(Geo g, int G, int ngroups, int nwords,
+                                                                   const uint32_t* __restrict__ bits,
+                                                                   const float2* __restrict__ norms,
+                                                                   uint32_t* __restrict__ ulq, int32_t* __restrict__ cntq,
+                                                                   uint32_t* __restrict__ ulk, int32_t* __restrict__ cntk,
+                                                                   int32_t* __restrict__ ordq, int32_t* __restrict__ ordk,
+                                                                   int* __restrict__ counters) {
     const int BH = g.B * g.H, nb = g.nb;
-    __shared__ float part[256];
+    __shared__ float part[LISTS_THREADS];
+    extern __shared__ int go_start[];   // [nb + 1], then the tiles' list lengths [ngroups]
+    int* cnt = go_start + nb + 1;
     pdl_launch_dependents();
     pdl_wait();
-    extern __shared__ int go_start[];   // [nb + 1]
     const int dir = static_cast<int>(blockIdx.x) / BH, bh = static_cast<int>(blockIdx.x) - dir * BH;
-    const int32_t* cnt = (dir ? cntk : cntq) + static_cast<long long>(bh) * ngroups;
-    int32_t* ord = (dir ? ordk : ordq) + static_cast<long long>(bh) * ngroups;
+    const long long unit0 = static_cast<long long>(bh) * ngroups;
+    int32_t* ord = (dir ? ordk : ordq) + unit0;
+    for (int u = threadIdx.x >> 5; u < ngroups; u += LISTS_THREADS / 32) {
+        const int n = grad_list(g, G, nwords, bits + static_cast<long long>(bh) * nb * nwords, dir != 0, u,
+                                (dir ? ulk : ulq) + (unit0 + u) * nb);
+        if ((threadIdx.x & 31) == 0) {
+            cnt[u] = n;
+            (dir ? cntk : cntq)[unit0 + u] = n;
+        }
+    }
     if (bh == 0 && threadIdx.x == 0) counters[dir] = 0;
     const int n8 = static_cast<int>(g.Npad / 8);
     norms += static_cast<long long>(bh) * n8;
     float limit = 0.f;
     if (dir == 0) {
         float v2 = 0.f;
-        for (int i = threadIdx.x; i < n8; i += 256) v2 += norms[i].y;
+        for (int i = threadIdx.x; i < n8; i += LISTS_THREADS) v2 += norms[i].y;
         part[threadIdx.x] = v2;
         __syncthreads();
-        for (int d = 128; d > 0; d >>= 1) {
+        for (int d = LISTS_THREADS / 2; d > 0; d >>= 1) {
             if (static_cast<int>(threadIdx.x) < d) part[threadIdx.x] += part[threadIdx.x + d];
             __syncthreads();
         }
@@ -1096,11 +1095,9 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
         g, stat_blocks, wl.nwords, static_cast<const uint4*>(o_t), static_cast<const uint4*>(do_t),
         static_cast<const uint4*>(v_t), lse, kv_idx, kv_cnt, nlse2, ndelta, norms, bits, ext);
     FV_CHECK_LAUNCH();
-    int rc = launch_after(grad_lists_kernel, static_cast<unsigned>((2ll * BH * wl.ngroups + 7) / 8), 256, 0, s, g, wl.G,
-                          wl.ngroups, wl.nwords, bits, ulq, cntq, ulk, cntk);
-    if (rc != FVATTN_OK) return rc;
-    rc = launch_after(grad_order_kernel, 2 * BH, 256, sizeof(int) * (g.nb + 1), s, g, wl.G, wl.ngroups, norms, cntq, cntk,
-                      ordq, ordk, counters);
+    int rc = launch_after(grad_lists_kernel, static_cast<unsigned>(2 * BH), LISTS_THREADS,
+                          sizeof(int) * (g.nb + 1 + wl.ngroups), s, g, wl.G, wl.ngroups, wl.nwords, bits, norms, ulq, cntq,
+                          ulk, cntk, ordq, ordk, counters);
     if (rc != FVATTN_OK) return rc;
 
     GradArgs a;
