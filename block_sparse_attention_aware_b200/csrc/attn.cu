@@ -1094,15 +1094,22 @@ template <int D, bool GRP, bool LSE>
 static int launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& args,
                        int grid, cudaStream_t s) {
     using L = Smem<D>;
-    if (cudaFuncSetAttribute(sparse_attn_kernel<D, GRP, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(L::ALLOC)) != cudaSuccess)
-        return FVATTN_ERR_CUDA;
-    // The warpgroups' register shares (setmaxnreg) must fit in what a CTA is
-    // launched with, or the raising warpgroups would wait for ever.
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, sparse_attn_kernel<D, GRP, LSE>) != cudaSuccess) return FVATTN_ERR_CUDA;
-    if (static_cast<long long>(fa.numRegs) * ATT_THREADS < 128ll * RegSplit<GRP>::LOW + 256ll * RegSplit<GRP>::HIGH)
-        return FVATTN_ERR_UNSUPPORTED;
+    static std::atomic<unsigned long long> ready{0};   // devices on which the kernel has its shared memory
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return FVATTN_ERR_CUDA;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if ((ready.load(std::memory_order_relaxed) & bit) == 0ull) {
+        if (cudaFuncSetAttribute(sparse_attn_kernel<D, GRP, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(L::ALLOC)) != cudaSuccess)
+            return FVATTN_ERR_CUDA;
+        // The warpgroups' register shares (setmaxnreg) must fit in what a CTA is
+        // launched with, or the raising warpgroups would wait for ever.
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, sparse_attn_kernel<D, GRP, LSE>) != cudaSuccess) return FVATTN_ERR_CUDA;
+        if (static_cast<long long>(fa.numRegs) * ATT_THREADS < 128ll * RegSplit<GRP>::LOW + 256ll * RegSplit<GRP>::HIGH)
+            return FVATTN_ERR_UNSUPPORTED;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     sparse_attn_kernel<D, GRP, LSE><<<grid, ATT_THREADS, L::ALLOC, s>>>(tq, tk, tv, args);
     FV_CHECK_LAUNCH();
     return FVATTN_OK;

@@ -637,20 +637,24 @@ static size_t attn_ws(int B, int Hq, int D, int parts) {
     return (n * 8 + 255) / 256 * 256 + n * D * 4;
 }
 
-static int current_sms() {
+// The current device and its SMs (148 without a device: sizes are asked for on
+// machines without one too).
+static int current_sms(int* device = nullptr) {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (device) *device = dev;
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
 template <int D, int NT>
-static int launch_cache_attn(const CUtensorMap& tk, const CUtensorMap& tv, const DecArgs& a, int B, int nsm,
+static int launch_cache_attn(const CUtensorMap& tk, const CUtensorMap& tv, const DecArgs& a, int B, int dev, int nsm,
                              cudaStream_t s) {
     using L = DecSmem<D>;
     static std::atomic<unsigned long long> ready{0};   // devices on which the kernel has its shared memory
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return FVATTN_ERR_CUDA;
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
     if ((ready.load(std::memory_order_relaxed) & bit) == 0ull) {
         if (cudaFuncSetAttribute(cache_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -784,7 +788,8 @@ extern "C" int fvattn_cache_attn(const fvattn_cache* c, int B, int Hq, const voi
     a.gchunks = (a.group + 15) / 16;
     if (static_cast<long long>(a.Hkv) * a.gchunks > 65535 || static_cast<long long>(B) * Hq > 0x7fffffffll)
         return FVATTN_ERR_UNSUPPORTED;
-    const int nsm = current_sms();
+    int dev = 0;
+    const int nsm = current_sms(&dev);
     a.B = B;
     a.parts = split_parts(B, Hq, c->Hkv, longest, nsm, &a.tokens);
     if (a.parts > 1) {
@@ -816,8 +821,8 @@ extern "C" int fvattn_cache_attn(const fvattn_cache* c, int B, int Hq, const voi
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool two = a.group > 8;
     if (c->D == 128)
-        return two ? launch_cache_attn<128, 2>(tk, tv, a, B, nsm, s) : launch_cache_attn<128, 1>(tk, tv, a, B, nsm, s);
-    return two ? launch_cache_attn<64, 2>(tk, tv, a, B, nsm, s) : launch_cache_attn<64, 1>(tk, tv, a, B, nsm, s);
+        return two ? launch_cache_attn<128, 2>(tk, tv, a, B, dev, nsm, s) : launch_cache_attn<128, 1>(tk, tv, a, B, dev, nsm, s);
+    return two ? launch_cache_attn<64, 2>(tk, tv, a, B, dev, nsm, s) : launch_cache_attn<64, 1>(tk, tv, a, B, dev, nsm, s);
 }
 
 int fv::take_status_cache() { return fv::take_tu_status(); }
