@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
+    pdl_wait();              // the work lists of the kernels before
 
     if (warp >= FIRST_SOFTMAX_WARP) {
         regs_inc<RegSplit<GRP>::HIGH>();
@@ -921,6 +922,7 @@ __global__ void __launch_bounds__(256) group_union_kernel(Geo g, int G, int ngro
                                                           const int32_t* __restrict__ kv_cnt,
                                                           uint32_t* __restrict__ ulist, int32_t* __restrict__ gcnt) {
     extern __shared__ uint32_t gb_smem[];   // [8 warps][G * nwords] membership bitmaps
+    pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long unit = static_cast<long long>(blockIdx.x) * 8 + warp;
     if (unit >= static_cast<long long>(g.B) * g.H * ngroups) return;
@@ -983,6 +985,8 @@ __global__ void __launch_bounds__(256) worklist_head_kernel(Geo g, int units, co
                                                             int32_t* __restrict__ item_order,
                                                             long long* __restrict__ head_cost) {
     extern __shared__ int wl_hist[];   // [nb + 2]
+    pdl_launch_dependents();
+    pdl_wait();
     const int nb = g.nb;
     const long long bh = blockIdx.x;
     const int32_t* cnt = cost_in + bh * units;
@@ -1025,6 +1029,8 @@ __global__ void __launch_bounds__(256) worklist_head_kernel(Geo g, int units, co
 __global__ void __launch_bounds__(256) worklist_heads_kernel(Geo g, int BH, const long long* __restrict__ head_cost,
                                                              int32_t* __restrict__ head_order, int* counter,
                                                              int32_t* __restrict__ ext) {
+    pdl_launch_dependents();
+    pdl_wait();              // (the attention kernel of the call before reads ext too)
     for (int b = threadIdx.x; b < g.nb; b += blockDim.x) ext[b] = block_extent(g, b);
     for (int h = threadIdx.x; h < BH; h += blockDim.x) {
         const long long ch = head_cost[h];
@@ -1110,9 +1116,8 @@ static int launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
             return FVATTN_ERR_UNSUPPORTED;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    sparse_attn_kernel<D, GRP, LSE><<<grid, ATT_THREADS, L::ALLOC, s>>>(tq, tk, tv, args);
-    FV_CHECK_LAUNCH();
-    return FVATTN_OK;
+    return launch_after(sparse_attn_kernel<D, GRP, LSE>, static_cast<unsigned>(grid), ATT_THREADS, L::ALLOC, s, tq, tk, tv,
+                        args);
 }
 
 }  // namespace fv
@@ -1167,12 +1172,18 @@ static int attn_impl(const fvattn_geom* gp, const void* q_t, const void* k_t, co
             g, wl.G, wl.ngroups, wl.nwords, lse ? 0 : 1, kv_idx, kv_cnt, ulist, gcnt);
         FV_CHECK_LAUNCH();
     }
-    worklist_head_kernel<<<BH, 256, sizeof(int) * (g.nb + 2), s>>>(g, units, wl.G > 1 ? gcnt : kv_cnt, item_order,
-                                                                   head_cost);
-    FV_CHECK_LAUNCH();
+    // without the union lists this is the call's first kernel, which waits for all of the stream before it
+    if (wl.G > 1) {
+        const int rc = launch_after(worklist_head_kernel, static_cast<unsigned>(BH), 256, sizeof(int) * (g.nb + 2), s, g,
+                                    units, gcnt, item_order, head_cost);
+        if (rc != FVATTN_OK) return rc;
+    } else {
+        worklist_head_kernel<<<BH, 256, sizeof(int) * (g.nb + 2), s>>>(g, units, kv_cnt, item_order, head_cost);
+        FV_CHECK_LAUNCH();
+    }
     int32_t* ext = reinterpret_cast<int32_t*>(ws + wl.ext);
-    worklist_heads_kernel<<<1, 256, 0, s>>>(g, BH, head_cost, head_order, counter, ext);
-    FV_CHECK_LAUNCH();
+    const int rc = launch_after(worklist_heads_kernel, 1, 256, 0, s, g, BH, head_cost, head_order, counter, ext);
+    if (rc != FVATTN_OK) return rc;
 
     CUtensorMap tq, tk, tv;
     if (!make_tmap(&tq, q_t, rows, g.D, g.bs) || !make_tmap(&tk, k_t, rows, g.D, g.bs) ||

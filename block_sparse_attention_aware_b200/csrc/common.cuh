@@ -49,6 +49,23 @@ static inline int take_tu_status() {
     return v;
 }
 
+// A launch that may begin while the stream's kernel before it ends; it waits
+// for that one's results itself (pdl_wait).
+template <class... P, class... A>
+static int launch_after(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA;
+}
+
 // The status words of the files whose kernels record errors.
 int take_status_route();
 int take_status_attn();

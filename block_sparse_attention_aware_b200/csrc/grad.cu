@@ -1021,23 +1021,6 @@ static GradWs grad_ws(const fvattn_geom& g) {
     return w;
 }
 
-// A launch that may begin while the stream's kernel before it ends; it waits
-// for that one's results itself (pdl_wait).
-template <class... P, class... A>
-static int launch_after(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA;
-}
-
 template <int D, bool KV>
 static int launch_grad(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
                        const GradArgs& args, int grid, int dev, cudaStream_t s) {
