@@ -30,7 +30,7 @@ int fvattn_sparse_attn_lse(const fvattn_geom *g, const void *q_t, const void *k_
                            void *workspace, size_t ws_bytes, fvattn_stream_t stream);
 
 /* Bytes of device workspace fvattn_sparse_attn_bwd needs: row statistics
- * (8 bytes a row), the block mask as bits, its lists by query tile and by
+ * (9 bytes a row), the block mask as bits, its lists by query tile and by
  * key tile (4 bytes per list slot: 2 x 70 MB for 40 heads at nb = 660) and
  * the work order.  0 for a null pointer. */
 size_t fvattn_sparse_attn_bwd_workspace_size(const fvattn_geom *g);
@@ -38,12 +38,17 @@ size_t fvattn_sparse_attn_bwd_workspace_size(const fvattn_geom *g);
 /* Gradients of fvattn_sparse_attn_lse with respect to Q, K and V.  With
  * P_tu = exp(scale * q_t . k_u - lse_t) on the kept real keys (0 elsewhere):
  *   dV_u = sum_t P_tu dO_t
- *   dS_tu = P_tu (dO_t . v_u - dO_t . O_t)
+ *   dS_tu = P_tu (dO_t . v_u - sum_w P_tw dO_t . v_w)
  *   dQ_t = scale * sum_u dS_tu k_u,   dK_u = scale * sum_t dS_tu q_t
  * The products run on the tensor cores in bf16 with fp32 accumulation (P and
- * dS are rounded to bf16 as operands); statistics and sums are fp32.  No
- * atomics touch a result: the output bits depend only on the inputs, not on
- * the schedule nor on how heads are split across calls.
+ * dS are rounded to bf16 as operands); statistics and sums are fp32.  The
+ * sum in dS is dO_t . O_t in exact arithmetic; it is formed from P where the
+ * bf16 O is too coarse for it.  No atomics touch a result: the output bits
+ * depend only on the inputs, not on the schedule nor on how heads are split
+ * across calls.  Blocks that no list holds are not read.  A NaN or infinity in
+ * a block reaches the rows and keys paired with it and, with blocks below 128
+ * tokens, those of the other blocks in the same 128 rows (as in
+ * fvattn_sparse_attn).
  *   q_t, k_t, v_t, do_t  [B, H, Npad, D] bf16 from fvattn_reorder (padding
  *                        rows zero)
  *   o_t, lse             as fvattn_sparse_attn_lse wrote them for the same
