@@ -239,7 +239,9 @@ class TrainLayer:
     inverse reorder of raster q, k, v, differentiable in q, k and v (the lists
     that routing picks are constants).  Every call has tiles, lists and
     statistics of its own, so several calls may be alive before their backward
-    passes, on one stream or several."""
+    passes, on one stream or several.  A step may be captured into a CUDA graph
+    with torch.autograd.grad on leaves that no living eager graph uses: drop
+    eager outputs before a capture."""
 
     def __init__(self, g: Geom, p: float, k: int, scale: Optional[float] = None, device="cuda", order: str = "raster"):
         if order not in ("raster", "hilbert"):
