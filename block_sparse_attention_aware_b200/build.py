@@ -6,7 +6,9 @@ Each .cu under csrc/ is compiled to an object with
 `-gencode arch=compute_100a,code=sm_100a -lineinfo -O3` as a whole program
 (no relocatable device code: ptxas honours per-warpgroup register budgets
 only then), then linked into block_sparse_attention_aware_b200/libfvattn.so.
-Needs only nvcc (no GPU).
+csrc/binding.cpp, a Python extension over that library's C ABI and torch's
+tensors, becomes _native.so beside it.  Needs nvcc, g++ and torch's headers (no
+GPU).
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfvattn.so")
+NATIVE = os.path.join(HERE, "_native.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 SOURCES = ["api.cu", "reorder.cu", "route.cu", "attn.cu", "noalloc.cu", "grad.cu", "cache.cu"]
@@ -33,8 +36,22 @@ def _deps():
     return max(os.path.getmtime(f) for f in files)
 
 
+def _native_command():
+    """g++ of binding.cpp against this interpreter's torch, to be linked with LIB."""
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    dirs = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(x for d in dirs for x in ("-isystem" if d != INCLUDE else "-I", d)), os.path.join(CSRC, "binding.cpp"),
+            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-L", HERE, "-l:libfvattn.so", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps():
+    if not force and all(os.path.exists(x) and os.path.getmtime(x) >= _deps() for x in (LIB, NATIVE)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     objs, procs = [], []
@@ -52,6 +69,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.check_call([NVCC, "-shared", "-gencode", "arch=compute_100a,code=sm_100a",
                            "-o", tmp, *objs, "-lcudart"])
     os.replace(tmp, LIB)
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    subprocess.check_call([*_native_command(), "-o", tmp])
+    os.replace(tmp, NATIVE)
     return LIB
 
 

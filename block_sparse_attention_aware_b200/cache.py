@@ -22,7 +22,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import fvattn
+from . import fvattn, train
 from .fvattn import _check
 from .train import _check_call, _need, _need_workspace, _on
 
@@ -139,6 +139,12 @@ class PagedCache:
         and lens[b] counts them.  With `rot` (rotation_table) and `pos`
         ([rows, len(axes)] int32) the keys, and the queries q ([rows, Hq, D])
         into q_out, are rotated; q_out may be q.  Returns q_out."""
+        if stream is None:
+            done = (train._fast or train.native()).append(
+                self.k_pages, self.v_pages, k, v, table, lens, cu, q, q_out, pos, rot,
+                None if axes is None else tuple(axes), bool(halves))
+            if done is not NotImplemented:
+                return done
         B, width = self._table(table)
         _vector("lens", lens, B, self.device)
         if cu is not None:
@@ -199,6 +205,12 @@ class PagedCache:
         query a sequence q [B, Hq, D] over its lens[b] cached tokens; Hq is a
         multiple of Hkv.  `longest`: no sequence is longer (default: what the
         table can hold; a nearer bound splits better)."""
+        if stream is None:
+            done = (train._fast or train.native()).attend(
+                self.k_pages, self.v_pages, q, table, lens, None if scale is None else float(scale),
+                None if longest is None else int(longest), out, lse, workspace)
+            if done is not NotImplemented:
+                return done
         B, width = self._table(table)
         _, hq, qs = self._rows("q", q, B, None)
         if hq % self.Hkv:

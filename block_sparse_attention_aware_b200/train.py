@@ -23,6 +23,17 @@ from .fvattn import Geom, _check, _raster
 EXPORTED = ("fvattn_sparse_attn_lse", "fvattn_sparse_attn_bwd_workspace_size", "fvattn_sparse_attn_bwd")
 
 _lib = None
+_fast = None      # the extension that serves a call's plain case (csrc/binding.cpp)
+
+
+def native():
+    """The extension over the C ABI, which checks and marshals a plain call in
+    2 us and answers NotImplemented to any other (raises if missing)."""
+    global _fast
+    if _fast is None:
+        from . import _native
+        _fast = _native
+    return _fast
 
 
 def load():
@@ -116,6 +127,11 @@ def sparse_attn_lse(g: Geom, qt, kt, vt, kv_idx, kv_cnt, scale: Optional[float] 
                     sm_stats: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
     """fvattn_sparse_attn_lse: (tiled O, lse [B, H, Npad] fp32).  A row with
     kv_cnt = 0 gets O = 0, lse = -inf.  `workspace` as fvattn.attn_workspace."""
+    if stream is None and sm_stats is None:
+        done = (_fast or native()).sparse_attn_lse(g, qt, kt, vt, kv_idx, kv_cnt, None if scale is None else float(scale),
+                                                   out, lse, workspace)
+        if done is not NotImplemented:
+            return done
     dev = _device("qt", qt)
     B, H, nb, Npad = g.B, g.H, g.nb, g.Npad
     tiled = (B, H, Npad, g.D)
@@ -161,6 +177,11 @@ def sparse_attn_bwd(g: Geom, qt, kt, vt, ot, dot, lse, kv_idx, kv_cnt, scale: Op
     """fvattn_sparse_attn_bwd: tiled (dQ, dK, dV) from the tensors of a
     sparse_attn_lse call and the tiled gradient `dot` of its output, whose
     padding rows are zero as fvattn.reorder writes them."""
+    if stream is None and dq is None and dk is None and dv is None:
+        done = (_fast or native()).sparse_attn_bwd(g, qt, kt, vt, ot, dot, lse, kv_idx, kv_cnt,
+                                                   None if scale is None else float(scale), workspace)
+        if done is not NotImplemented:
+            return done
     dev = _device("qt", qt)
     B, H, nb, Npad = g.B, g.H, g.nb, g.Npad
     tiled = (B, H, Npad, g.D)

@@ -287,3 +287,29 @@ def test_cache_refusals_on_the_gpu(fv, ca):  # noqa: F811
     with pytest.raises(ValueError, match="unsupported"):
         ca.PagedCache(*(torch.zeros((2, 2, 24, 64), dtype=BF16, device="cuda") for _ in range(2)))
     assert fv.get_status() == 0
+
+
+def test_both_ways_through_the_binding_agree(fv, ca):  # noqa: F811
+    """Without a stream argument a call is checked and marshalled by the extension, with one by the Python code."""
+    here = torch.cuda.current_stream()
+    c, table, ln = pool(ca, [300, 7, 0], 2, 64, 16, 3)
+    q, k, v = normal((3, 8, 64), 1), normal((3, 2, 64), 2), normal((3, 2, 64), 3)
+    rot, pos = ca.rotation_table(64, (20, 12), 50), torch.randint(0, 50, (3, 2), dtype=I32, device="cuda")
+    ln[2] = 1
+    table[2, 0] = c.pages - 1
+    for kw in (dict(), dict(scale=0.3, longest=400), dict(out=torch.empty_like(q), lse=torch.empty((3, 8), device="cuda")),
+               dict(workspace=c.attend_workspace(3, 8, 512), longest=512)):
+        a = [t.clone() for t in c.attend(q, table, ln, **kw)]
+        b = c.attend(q, table, ln, stream=here, **kw)
+        assert torch.equal(bits(a[0]), bits(b[0])) and torch.equal(a[1], b[1])
+    for kw in (dict(), dict(q=q), dict(q=q, q_out=torch.empty_like(q), rot=rot, pos=pos, axes=(20, 12), halves=True),
+               dict(rot=rot, pos=pos, axes=[20, 12]), dict(cu=torch.tensor([0, 1, 1, 3], dtype=I32, device="cuda"))):
+        ways = []
+        for extra in (dict(), dict(stream=here)):
+            c.k_pages.zero_(), c.v_pages.zero_()
+            out = c.append(k, v, table, ln + 2, **kw, **extra)
+            ways.append((c.k_pages.clone(), c.v_pages.clone(), None if out is None else out.clone()))
+        assert (ways[0][2] is None) == (ways[1][2] is None) == ("q" not in kw)
+        for x, y in zip(*ways):
+            assert x is None or torch.equal(bits(x), bits(y))
+    assert fv.get_status() == 0

@@ -327,3 +327,22 @@ def test_refusals_on_the_gpu(fv, tr):  # noqa: F811
         tr.attention(fv.with_order(g, fv.block_order(g)), *(torch.zeros((g.B, g.N, g.H, g.D), dtype=BF16, device="cuda"),) * 3,
                      idx, cnt)
     assert fv.get_status() == 0
+
+
+def test_both_ways_through_the_binding_agree(fv, tr):  # noqa: F811
+    """Without a stream argument a call is checked and marshalled by the extension, with one by the Python code."""
+    g = fv.geom(*GEO64)
+    idx, cnt = random_lists(g, 0.6, 4)
+    q, k, v, do = tiles(g, 5)
+    here = torch.cuda.current_stream()
+    for kw in (dict(), dict(scale=0.2)):
+        a, b = tr.sparse_attn_lse(g, q, k, v, idx, cnt, **kw), tr.sparse_attn_lse(g, q, k, v, idx, cnt, stream=here, **kw)
+        assert torch.equal(bits(a[0]), bits(b[0])) and torch.equal(a[1], b[1])
+        x = tr.sparse_attn_bwd(g, q, k, v, a[0], do, a[1], idx, cnt, **kw)
+        y = tr.sparse_attn_bwd(g, q, k, v, a[0], do, a[1], idx, cnt, stream=here, **kw)
+        for s, t in zip(x, y):
+            assert torch.equal(bits(s), bits(t))
+    out, lse = torch.empty_like(q), torch.empty_like(a[1])
+    got = tr.sparse_attn_lse(g, q, k, v, idx, cnt, scale=0.2, out=out, lse=lse, workspace=fv.attn_workspace(g))
+    assert got[0] is out and got[1] is lse and torch.equal(bits(out), bits(a[0]))
+    assert fv.get_status() == 0

@@ -201,3 +201,14 @@ def test_rotation_table_keeps_the_phase_of_far_positions(mods):
             # the angle itself is a 64-bit product of two roundings: 3 * 2^-53 * 10^6 more
             assert abs(t[n, i].item() - math.cos(a)) <= 2 ** -24 + 1e-9
             assert abs(t[n, 32 + i].item() - math.sin(a)) <= 2 ** -24 + 1e-9
+
+
+def test_the_extension_leaves_all_but_the_plain_case_to_the_bindings(mods):
+    fv, tr, _ = mods
+    n = tr.native()
+    t = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
+    g = fv.geom(1, 2, 64, 2, 8, 8, 2, 2, 4)
+    for f, count in ((n.append, 13), (n.attend, 10), (n.sparse_attn_lse, 10), (n.sparse_attn_bwd, 11)):
+        assert f() is NotImplemented and f(*[None] * count) is NotImplemented and f(*[1] * count) is NotImplemented
+        assert f(*[t] * count) is NotImplemented                       # not on a GPU
+        assert f(g, *[t] * (count - 1)) is NotImplemented
