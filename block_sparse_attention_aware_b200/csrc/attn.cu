@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
     // The 128-byte swizzle of TMA and of the tcgen05 operand descriptors
     // needs 1024-byte aligned tiles.
     if (smem_u32(smem) & 1023u) {
+        pdl_wait();
         if (threadIdx.x == 0) record_status(FVATTN_ERR_UNSUPPORTED);
         return;
     }
@@ -923,6 +924,7 @@ __global__ void __launch_bounds__(256) group_union_kernel(Geo g, int G, int ngro
                                                           uint32_t* __restrict__ ulist, int32_t* __restrict__ gcnt) {
     extern __shared__ uint32_t gb_smem[];   // [8 warps][G * nwords] membership bitmaps
     pdl_launch_dependents();
+    pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long unit = static_cast<long long>(blockIdx.x) * 8 + warp;
     if (unit >= static_cast<long long>(g.B) * g.H * ngroups) return;
@@ -930,19 +932,25 @@ __global__ void __launch_bounds__(256) group_union_kernel(Geo g, int G, int ngro
     const long long bh = unit / ngroups;
     const int grp = static_cast<int>(unit - bh * ngroups);
     uint32_t* bits = gb_smem + warp * G * nwords;
+    // the rows' counts and the first 32 entries of each list (junk past its count) are loaded side by side
+    const int nq = min(G, nb - grp * G);
+    const int32_t* lists = kv_idx + (bh * nb + grp * G) * nb;
+    int n = 0, first[MAX_GROUP];
+    if (lane < nq) n = kv_cnt[bh * nb + grp * G + lane];
+#pragma unroll
+    for (int t = 0; t < MAX_GROUP; ++t) first[t] = t < nq && lane < nb ? lists[static_cast<long long>(t) * nb + lane] : 0;
     for (int i = lane; i < G * nwords; i += 32) bits[i] = 0u;
+    if (lane < nq && (n < min_cnt || n > nb)) {
+        record_status(FVATTN_ERR_BOUNDS);
+        n = n < min_cnt ? min_cnt : nb;
+    }
     __syncwarp();
-    for (int t = 0; t < G; ++t) {
-        const int qb = grp * G + t;
-        if (qb >= nb) break;
-        int cnt = kv_cnt[bh * nb + qb];
-        if (cnt < min_cnt || cnt > nb) {
-            if (lane == 0) record_status(FVATTN_ERR_BOUNDS);
-            cnt = cnt < min_cnt ? min_cnt : nb;
-        }
-        const int32_t* list = kv_idx + (bh * nb + qb) * nb;
+#pragma unroll
+    for (int t = 0; t < MAX_GROUP; ++t) {
+        const int cnt = __shfl_sync(0xffffffffu, n, t);   // 0 past the last query block
+        const int32_t* list = lists + static_cast<long long>(t) * nb;
         for (int e = lane; e < cnt; e += 32) {
-            int j = list[e];
+            int j = e < 32 ? first[t] : list[e];
             if (j < 0 || j >= nb) {
                 record_status(FVATTN_ERR_BOUNDS);
                 j = 0;
@@ -1168,21 +1176,16 @@ static int attn_impl(const fvattn_geom* gp, const void* q_t, const void* k_t, co
 
     if (wl.G > 1) {
         const long long warps = static_cast<long long>(BH) * wl.ngroups;
-        group_union_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, sizeof(uint32_t) * 8 * wl.G * wl.nwords, s>>>(
-            g, wl.G, wl.ngroups, wl.nwords, lse ? 0 : 1, kv_idx, kv_cnt, ulist, gcnt);
-        FV_CHECK_LAUNCH();
-    }
-    // without the union lists this is the call's first kernel, which waits for all of the stream before it
-    if (wl.G > 1) {
-        const int rc = launch_after(worklist_head_kernel, static_cast<unsigned>(BH), 256, sizeof(int) * (g.nb + 2), s, g,
-                                    units, gcnt, item_order, head_cost);
+        const int rc = launch_after(group_union_kernel, static_cast<unsigned>((warps + 7) / 8), 256,
+                                    sizeof(uint32_t) * 8 * wl.G * wl.nwords, s, g, wl.G, wl.ngroups, wl.nwords, lse ? 0 : 1,
+                                    kv_idx, kv_cnt, ulist, gcnt);
         if (rc != FVATTN_OK) return rc;
-    } else {
-        worklist_head_kernel<<<BH, 256, sizeof(int) * (g.nb + 2), s>>>(g, units, kv_cnt, item_order, head_cost);
-        FV_CHECK_LAUNCH();
     }
+    int rc = launch_after(worklist_head_kernel, static_cast<unsigned>(BH), 256, sizeof(int) * (g.nb + 2), s, g, units,
+                          wl.G > 1 ? gcnt : kv_cnt, item_order, head_cost);
+    if (rc != FVATTN_OK) return rc;
     int32_t* ext = reinterpret_cast<int32_t*>(ws + wl.ext);
-    const int rc = launch_after(worklist_heads_kernel, 1, 256, 0, s, g, BH, head_cost, head_order, counter, ext);
+    rc = launch_after(worklist_heads_kernel, 1, 256, 0, s, g, BH, head_cost, head_order, counter, ext);
     if (rc != FVATTN_OK) return rc;
 
     CUtensorMap tq, tk, tv;

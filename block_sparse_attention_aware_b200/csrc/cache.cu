@@ -59,6 +59,8 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
     __shared__ long long s_row;          // first element of the token's row in its page (head 0)
     const long long t = blockIdx.x;
     const int tid = threadIdx.x;
+    pdl_launch_dependents();
+    pdl_wait();
     bool bad = false;                    // a position outside the rotation table
     if (tid < 32) {
         // the token's sequence: how many sequences end at or before it
@@ -234,6 +236,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DEC_CTAS)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
     if (sbase & 1023u) {   // the 128-byte swizzle needs 1024-byte aligned tiles
+        pdl_wait();
         if (threadIdx.x == 0) record_status(FVATTN_ERR_UNSUPPORTED);
         return;
     }
@@ -262,6 +265,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DEC_CTAS)
         fence_mbar_init();
     }
     __syncthreads();
+    pdl_wait();
     const int HG = a.Hkv * a.gchunks;
 
     if (warp == DEC_WARPS) {
@@ -670,22 +674,12 @@ static int launch_cache_attn(const CUtensorMap& tk, const CUtensorMap& tv, const
     }
     const long long items = static_cast<long long>(B) * a.Hkv * a.gchunks * a.parts;
     const long long slots = static_cast<long long>(nsm) * DEC_CTAS;
-    cache_attn_kernel<D, NT><<<static_cast<unsigned>(items < slots ? items : slots), DEC_THREADS, L::TOTAL, s>>>(tk, tv, a);
-    FV_CHECK_LAUNCH();
-    if (a.parts == 1) return FVATTN_OK;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(B) * static_cast<unsigned>(a.Hq));
-    cfg.blockDim = dim3(a.parts > 32 ? 512 : 128);
-    cfg.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = a.parts > 32 ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, 16>, a)
-                                       : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, 4>, a);
-    if (e != cudaSuccess) return FVATTN_ERR_CUDA;
-    return FVATTN_OK;
+    const int rc = launch_after(cache_attn_kernel<D, NT>, dim3(static_cast<unsigned>(items < slots ? items : slots)), DEC_THREADS,
+                                L::TOTAL, s, tk, tv, a);
+    if (rc != FVATTN_OK || a.parts == 1) return rc;
+    const dim3 heads(static_cast<unsigned>(B) * static_cast<unsigned>(a.Hq));
+    return a.parts > 32 ? launch_after(cache_join_kernel<D, 16>, heads, 512, 0, s, a)
+                        : launch_after(cache_join_kernel<D, 4>, heads, 128, 0, s, a);
 }
 
 }  // namespace fv
@@ -754,12 +748,8 @@ extern "C" int fvattn_cache_append(const fvattn_cache* c, int B, long long rows,
     const int passes = (a.Hq + 2 * a.Hkv + per - 1) / per;
     const dim3 grid(static_cast<unsigned>(rows), rows < 512 ? static_cast<unsigned>(passes < 64 ? passes : 64) : 1u);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (c->D == 128)
-        cache_append_kernel<128><<<grid, 256, 0, s>>>(a);
-    else
-        cache_append_kernel<64><<<grid, 256, 0, s>>>(a);
-    FV_CHECK_LAUNCH();
-    return FVATTN_OK;
+    return c->D == 128 ? launch_after(cache_append_kernel<128>, grid, 256, 0, s, a)
+                       : launch_after(cache_append_kernel<64>, grid, 256, 0, s, a);
 }
 
 extern "C" int fvattn_cache_attn_parts(int B, int Hq, int Hkv, int D, long long longest, int* tokens) {

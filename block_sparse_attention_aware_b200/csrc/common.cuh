@@ -49,12 +49,13 @@ static inline int take_tu_status() {
     return v;
 }
 
-// A launch that may begin while the stream's kernel before it ends; it waits
-// for that one's results itself (pdl_wait).
+// A launch that may begin while the stream's kernel before it ends.  Every
+// kernel launched so touches no memory before pdl_wait, in which each of its
+// threads waits for that one's end and results.
 template <class... P, class... A>
-static int launch_after(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
+static int launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;

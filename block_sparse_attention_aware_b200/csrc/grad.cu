@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
     constexpr int NS0 = GRAD_STAGES0, NS1 = GRAD_STAGES1;
     extern __shared__ __align__(1024) unsigned char smem[];
     if (smem_u32(smem) & 1023u) {   // the 128-byte swizzle needs 1024-byte aligned tiles
+        pdl_wait();
         if (threadIdx.x == 0) record_status(FVATTN_ERR_UNSUPPORTED);
         return;
     }
@@ -798,6 +799,7 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, 
                                                         int32_t* __restrict__ ext) {
     extern __shared__ uint32_t gp_bits[];   // [8][nwords]
     pdl_launch_dependents();
+    pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (static_cast<int>(blockIdx.x) < stat_blocks) {
         constexpr int LPR = D / 8;           // lanes a row
@@ -1086,11 +1088,12 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
 
     const int stat_blocks = static_cast<int>((rows + 63) / 64);
     const int bit_blocks = static_cast<int>((static_cast<long long>(BH) * g.nb + 7) / 8);
-    grad_prep_kernel<D><<<stat_blocks + bit_blocks, 256, sizeof(uint32_t) * 8 * wl.nwords, s>>>(
-        g, stat_blocks, wl.nwords, static_cast<const uint4*>(o_t), static_cast<const uint4*>(do_t),
-        static_cast<const uint4*>(v_t), lse, kv_idx, kv_cnt, nlse2, ndelta, norms, bits, ext);
-    FV_CHECK_LAUNCH();
-    int rc = launch_after(grad_lists_kernel, static_cast<unsigned>(2 * BH), LISTS_THREADS,
+    int rc = launch_after(grad_prep_kernel<D>, static_cast<unsigned>(stat_blocks + bit_blocks), 256,
+                          sizeof(uint32_t) * 8 * wl.nwords, s, g, stat_blocks, wl.nwords, static_cast<const uint4*>(o_t),
+                          static_cast<const uint4*>(do_t), static_cast<const uint4*>(v_t), lse, kv_idx, kv_cnt, nlse2,
+                          ndelta, norms, bits, ext);
+    if (rc != FVATTN_OK) return rc;
+    rc = launch_after(grad_lists_kernel, static_cast<unsigned>(2 * BH), LISTS_THREADS,
                           sizeof(int) * (g.nb + 1 + wl.ngroups), s, g, wl.G, wl.ngroups, wl.nwords, bits, norms, ulq, cntq,
                           ulk, cntk, ordq, ordk, counters);
     if (rc != FVATTN_OK) return rc;

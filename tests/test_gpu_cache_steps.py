@@ -313,3 +313,45 @@ def test_both_ways_through_the_binding_agree(fv, ca):  # noqa: F811
         for x, y in zip(*ways):
             assert x is None or torch.equal(bits(x), bits(y))
     assert fv.get_status() == 0
+
+
+def test_capture_behind_copies_fills_and_another_stream(fv, ca):  # noqa: F811
+    """The calls' first kernels may start while the work before them ends: behind a copy, a fill and an event of
+    another stream, in a graph, they wait for it all the same."""
+    c, table, ln = pool(ca, [90, 200], 2, 64, 16, 3)
+    src = [normal((2, 2, 64), s) for s in (1, 2)] + [normal((2, 8, 64), 3)]
+    k, v, q = (torch.zeros_like(t) for t in src)
+    o, lse = torch.empty_like(q), torch.empty((2, 8), device="cuda")
+    ws = c.attend_workspace(2, 8, 300)
+    other = torch.cuda.Stream()
+
+    def step():
+        k.copy_(src[0])
+        c.k_pages.fill_(0.5)
+        side = torch.cuda.current_stream()
+        other.wait_stream(side)
+        with torch.cuda.stream(other):
+            v.copy_(src[1])
+            c.v_pages.fill_(0.25)
+            q.copy_(src[2])
+        side.wait_stream(other)
+        c.append(k, v, table, ln)
+        c.attend(q, table, ln, longest=300, out=o, lse=lse, workspace=ws)
+        return c.k_pages.sum(), o.float().sum()
+
+    step()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (c.k_pages, c.v_pages, o, lse)]
+    check_attend((o, lse), attend_definition(c, q, table, ln, 0.125))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sums = step()
+    for t in (k, v, q, o, lse, c.k_pages, c.v_pages):
+        t.zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, (c.k_pages, c.v_pages, o, lse)):
+        assert torch.equal(a, b)
+    assert torch.equal(sums[0], c.k_pages.sum()) and torch.equal(sums[1], o.float().sum())
+    assert fv.get_status() == 0
