@@ -83,7 +83,9 @@ constexpr int GRAD_THREADS = 128 * (1 + GRAD_GROUPS);
 constexpr int GRAD_STAGES0 = 3, GRAD_STAGES1 = 2;
 constexpr uint32_t GRAD_TMEM = 512;
 constexpr float GRAD_EXACT = 1.f / 16.f;
-constexpr int GRAD_FLAG = 1 << 30;   // in the work order: a query tile that needs the exact delta
+// An entry of the work order: tile | its list's length << 12 | GRAD_FLAG if it is a query tile that needs the
+// exact delta (at most 2560 blocks: 12 bits each).
+constexpr int GRAD_FLAG = 1 << 30;
 constexpr int GRAD_GROUP = 8;     // blocks per tile at bs = 16
 // Register split (setmaxnreg): the launch gives 96 a thread; one warpgroup
 // of producers and issuers at LOW, the arithmetic at HIGH.
@@ -97,8 +99,7 @@ struct GradArgs {
     Geo g;
     int G, ngroups;
     const uint32_t* ul;       // [B*H][ngroups][nb] this pass's lists: block | membership bits << 24
-    const int32_t* cnt;       // [B*H][ngroups] their lengths
-    const int32_t* order;     // [B*H][ngroups] tiles of a head, longest first; with GRAD_FLAG
+    const int32_t* order;     // [B*H][ngroups] a head's tiles, longest list first
     int* counter;
     const int32_t* ext;       // [nb] real extent of each block
     const float* nlse2;       // [B*H][Npad] -lse * log2(e); -inf for rows that take no part
@@ -498,9 +499,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
             while (ok) {
                 const int slot = item_seq & 1;
                 if (!wait_warp(smem_u32(&ctl.item_empty[slot]), ((item_seq >> 1) & 1) ^ 1, abort_flag, wlim)) break;
-                int t = 0;
-                if (lane == 0) t = atomicAdd(a.counter, 1);
-                t = __shfl_sync(0xffffffffu, t, 0);
+                int t = static_cast<int>(blockIdx.x);          // the first; then the next that nobody has taken
+                if (item_seq > 0) {
+                    if (lane == 0) t = atomicAdd(a.counter, 1) + static_cast<int>(gridDim.x);
+                    t = __shfl_sync(0xffffffffu, t, 0);
+                }
                 if (t >= a.total_items) {
                     if (lane == 0) {
                         ctl.item[slot][3] = 0;
@@ -510,9 +513,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 }
                 const int bh = t / a.ngroups;
                 const int entry = __ldg(a.order + t);
-                const int u = entry & (GRAD_FLAG - 1);
+                const int u = entry & 0xFFF, cnt = (entry >> 12) & 0xFFF;
                 const long long unit = static_cast<long long>(bh) * a.ngroups + u;
-                const int cnt = __ldg(a.cnt + unit);
                 if (lane == 0) {
                     ctl.item[slot][0] = bh;
                     ctl.item[slot][1] = u;
@@ -539,11 +541,18 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                     }
                 }
                 const uint32_t* ul = a.ul + unit * g.nb;
+                // a chunk's blocks, membership bits and real extents are looked up a chunk ahead
+                uint32_t m_next = 0u;
+                int j_next = lane < bpc ? grad_slot(ul, lane, cnt, m_next) : -1;
+                int e_next = !KV && j_next >= 0 ? __ldg(a.ext + j_next) : 0;
                 for (int i = 0; i < nc; ++i, ++c) {
                     const int st = c % NS0;
-                    uint32_t mem = 0u;
-                    const int j = lane < bpc ? grad_slot(ul, i * bpc + lane, cnt, mem) : -1;
-                    const int ext = !KV && j >= 0 ? __ldg(a.ext + j) : 0;
+                    const uint32_t mem = m_next;
+                    const int j = j_next, ext = e_next;
+                    if (i + 1 < nc) {
+                        j_next = lane < bpc ? grad_slot(ul, (i + 1) * bpc + lane, cnt, m_next) : -1;
+                        e_next = !KV && j_next >= 0 ? __ldg(a.ext + j_next) : 0;
+                    }
                     if (!wait_warp(smem_u32(&ctl.b0_empty[st]), ((c / NS0) & 1) ^ 1, abort_flag, wlim)) {
                         ok = false;
                         break;
@@ -609,10 +618,12 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 const int nc = (cnt + bpc - 1) / bpc;
                 const int row_base = bh * static_cast<int>(g.Npad);
                 const uint32_t* ul = a.ul + (static_cast<long long>(bh) * a.ngroups + u) * g.nb;
+                uint32_t mem = 0u;
+                int j_next = lane < bpc ? grad_slot(ul, lane, cnt, mem) : -1;
                 for (int i = 0; i < nc; ++i, ++c) {
                     const int st = c % NS1;
-                    uint32_t mem = 0u;
-                    const int j = lane < bpc ? grad_slot(ul, i * bpc + lane, cnt, mem) : -1;
+                    const int j = j_next;
+                    if (i + 1 < nc) j_next = lane < bpc ? grad_slot(ul, (i + 1) * bpc + lane, cnt, mem) : -1;
                     if (!wait_warp(smem_u32(&ctl.b1_empty[st]), ((c / NS1) & 1) ^ 1, abort_flag, wlim)) {
                         ok = false;
                         break;
@@ -936,8 +947,7 @@ constexpr int LISTS_THREADS = 1024;
 __global__ void __launch_bounds__(LISTS_THREADS) grad_lists_kernel(Geo g, int G, int ngroups, int nwords,
                                                                    const uint32_t* __restrict__ bits,
                                                                    const float2* __restrict__ norms,
-                                                                   uint32_t* __restrict__ ulq, int32_t* __restrict__ cntq,
-                                                                   uint32_t* __restrict__ ulk, int32_t* __restrict__ cntk,
+                                                                   uint32_t* __restrict__ ulq, uint32_t* __restrict__ ulk,
                                                                    int32_t* __restrict__ ordq, int32_t* __restrict__ ordk,
                                                                    int* __restrict__ counters) {
     const int BH = g.B * g.H, nb = g.nb;
@@ -952,10 +962,7 @@ __global__ void __launch_bounds__(LISTS_THREADS) grad_lists_kernel(Geo g, int G,
     for (int u = threadIdx.x >> 5; u < ngroups; u += LISTS_THREADS / 32) {
         const int n = grad_list(g, G, nwords, bits + static_cast<long long>(bh) * nb * nwords, dir != 0, u,
                                 (dir ? ulk : ulq) + (unit0 + u) * nb);
-        if ((threadIdx.x & 31) == 0) {
-            cnt[u] = n;
-            (dir ? cntk : cntq)[unit0 + u] = n;
-        }
+        if ((threadIdx.x & 31) == 0) cnt[u] = n;
     }
     if (bh == 0 && threadIdx.x == 0) counters[dir] = 0;
     const int n8 = static_cast<int>(g.Npad / 8);
@@ -993,7 +1000,7 @@ __global__ void __launch_bounds__(LISTS_THREADS) grad_lists_kernel(Geo g, int G,
     }
     __syncthreads();
     for (int i = threadIdx.x; i < ngroups; i += blockDim.x) {
-        int entry = i;
+        int entry = i | (cnt[i] << 12);
         if (dir == 0) {
             const int at = i * G * g.bs / 8, n = min(G * g.bs / 8, n8 - at);
             float o2 = 0.f;
@@ -1007,7 +1014,7 @@ __global__ void __launch_bounds__(LISTS_THREADS) grad_lists_kernel(Geo g, int G,
 // ------------------------------------------------------------------ host side
 
 struct GradWs {
-    size_t nlse2, ndelta, norms, bits, ulq, ulk, cntq, cntk, ordq, ordk, ext, counters, total;
+    size_t nlse2, ndelta, norms, bits, ulq, ulk, ordq, ordk, ext, counters, total;
     int G, ngroups, nwords;
 };
 
@@ -1025,9 +1032,7 @@ static GradWs grad_ws(const fvattn_geom& g) {
     w.bits = w.norms + al(BH * g.Npad);
     w.ulq = w.bits + al(4 * BH * nb * w.nwords);
     w.ulk = w.ulq + al(4 * units * nb);
-    w.cntq = w.ulk + al(4 * units * nb);
-    w.cntk = w.cntq + al(4 * units);
-    w.ordq = w.cntk + al(4 * units);
+    w.ordq = w.ulk + al(4 * units * nb);
     w.ordk = w.ordq + al(4 * units);
     w.ext = w.ordk + al(4 * units);
     w.counters = w.ext + al(4 * nb);
@@ -1068,8 +1073,6 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
     uint32_t* bits = reinterpret_cast<uint32_t*>(ws + wl.bits);
     uint32_t* ulq = reinterpret_cast<uint32_t*>(ws + wl.ulq);
     uint32_t* ulk = reinterpret_cast<uint32_t*>(ws + wl.ulk);
-    int32_t* cntq = reinterpret_cast<int32_t*>(ws + wl.cntq);
-    int32_t* cntk = reinterpret_cast<int32_t*>(ws + wl.cntk);
     int32_t* ordq = reinterpret_cast<int32_t*>(ws + wl.ordq);
     int32_t* ordk = reinterpret_cast<int32_t*>(ws + wl.ordk);
     int32_t* ext = reinterpret_cast<int32_t*>(ws + wl.ext);
@@ -1094,8 +1097,8 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
                           ndelta, norms, bits, ext);
     if (rc != FVATTN_OK) return rc;
     rc = launch_after(grad_lists_kernel, static_cast<unsigned>(2 * BH), LISTS_THREADS,
-                          sizeof(int) * (g.nb + 1 + wl.ngroups), s, g, wl.G, wl.ngroups, wl.nwords, bits, norms, ulq, cntq,
-                          ulk, cntk, ordq, ordk, counters);
+                          sizeof(int) * (g.nb + 1 + wl.ngroups), s, g, wl.G, wl.ngroups, wl.nwords, bits, norms, ulq,
+                          ulk, ordq, ordk, counters);
     if (rc != FVATTN_OK) return rc;
 
     GradArgs a;
@@ -1112,7 +1115,6 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
     a.wait_limit_ns = WAIT_LIMIT_NS;
     const int grid = nsm < a.total_items ? nsm : a.total_items;
     a.ul = ulq;
-    a.cnt = cntq;
     a.order = ordq;
     a.counter = counters;
     a.out0 = static_cast<__nv_bfloat16*>(dq_t);
@@ -1120,7 +1122,6 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
     rc = launch_grad<D, false>(tq, tdo, tk, tv, a, grid, dev, s);
     if (rc != FVATTN_OK) return rc;
     a.ul = ulk;
-    a.cnt = cntk;
     a.order = ordk;
     a.counter = counters + 1;
     a.out0 = static_cast<__nv_bfloat16*>(dv_t);
