@@ -175,6 +175,11 @@ __device__ __forceinline__ uint32_t grad_mask(const uint32_t* m, int lbs, int tb
     return all ? mw : mw & pad;
 }
 
+// Which of a chunk's columns a warp's rows see: the arithmetic's three bodies.
+enum GradColumns { ALL, SOME, NOTHING };
+template <GradColumns C>
+using Body = std::integral_constant<GradColumns, C>;
+
 template <int D, bool KV>
 __global__ void __launch_bounds__(GRAD_THREADS, 1)
     grad_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
@@ -305,15 +310,19 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 uint32_t pv[32];                    // S, then P, of this row
                 tmem_ld32(sbuf, pv);
                 uint32_t mw = grad_mask(ctl.mask[st0], lbs, tb, w, all);   // columns that the row sees
-                const bool full = __all_sync(0xffffffffu, mw == 0xFFFFFFFFu);
+                const bool full = __all_sync(0xffffffffu, mw == 0xFFFFFFFFu), none = __all_sync(0xffffffffu, mw == 0u);
                 tmem_wait_ld();
-                // The whole chunk's arithmetic is there twice: without masks, and with a select an element.
-                // One body that tests for masks on the way took twice the time, masks or not.
-                auto chunk = [&](auto without_masks, auto with_a0) {
-                    constexpr bool FULL = decltype(without_masks)::value, TWO = decltype(with_a0)::value;
+                // The chunk's arithmetic is there without masks, with a select an element, and for rows that see
+                // none of its columns (with blocks of 32 or more one of the first and last holds for a whole
+                // warp).  One body that tests for masks on the way took twice the time, masks or not.
+                auto chunk = [&](auto body, auto with_a0) {
+                    constexpr bool FULL = decltype(body)::value == ALL, NONE = decltype(body)::value == NOTHING;
+                    constexpr bool TWO = decltype(with_a0)::value;
                     // several bodies for the compiler too, which else moves the loads of all before the branch
                     if constexpr (FULL)
                         asm volatile("// every column" ::: "memory");
+                    else if constexpr (NONE)
+                        asm volatile("// no column" ::: "memory");
                     else
                         asm volatile("// masks" ::: "memory");
                     if constexpr (!TWO) {
@@ -335,12 +344,14 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                             if (KV) add = nls[e >> 2];
 #pragma unroll
                             for (int z = 0; z < 4; z += 2) {
-                                float x0, x1;
-                                f2_unpack(f2_fma(f2_pack(__uint_as_float(pv[e + z]), __uint_as_float(pv[e + z + 1])), sl2x2,
-                                                 z ? add.y : add.x), x0, x1);
-                                x0 = ex2_approx(x0);
-                                x1 = ex2_approx(x1);
-                                if (!FULL) {
+                                float x0 = 0.f, x1 = 0.f;
+                                if (!NONE) {
+                                    f2_unpack(f2_fma(f2_pack(__uint_as_float(pv[e + z]), __uint_as_float(pv[e + z + 1])),
+                                                     sl2x2, z ? add.y : add.x), x0, x1);
+                                    x0 = ex2_approx(x0);
+                                    x1 = ex2_approx(x1);
+                                }
+                                if (!FULL && !NONE) {
                                     x0 = (mw & (1u << (e + z))) ? x0 : 0.f;
                                     x1 = (mw & (1u << (e + z + 1))) ? x1 : 0.f;
                                 }
@@ -369,8 +380,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                     }
                     tc_fence_after();
                     uint32_t dv[32], ds[16];
-                    tmem_ld32(dpbuf, dv);
-                    tmem_wait_ld();
+                    if (!NONE) {
+                        tmem_ld32(dpbuf, dv);
+                        tmem_wait_ld();
+                    }
                     // (the bits' tests are made again: kept from above they would take 32 registers)
                     if (!FULL) asm volatile("" : "+r"(mw));
                     const ulonglong2* nds = reinterpret_cast<const ulonglong2*>(&ctl.stat[NS0 + st1][w * 32]);
@@ -380,6 +393,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                         if (KV) add = nds[e >> 2];
 #pragma unroll
                         for (int z = 0; z < 4; z += 2) {
+                            if (NONE) {
+                                ds[(e + z) >> 1] = 0u;
+                                continue;
+                            }
                             float x0 = __uint_as_float(dv[e + z]), x1 = __uint_as_float(dv[e + z + 1]);
                             if (!FULL && !KV) {   // nothing of a masked pair enters the sum
                                 x0 = (mw & (1u << (e + z))) ? x0 : 0.f;
@@ -406,10 +423,15 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                     }
                     return true;
                 };
+                auto either = [&](auto with_a0) {
+                    return full   ? chunk(Body<ALL>{}, with_a0)
+                           : none ? chunk(Body<NOTHING>{}, with_a0)
+                                  : chunk(Body<SOME>{}, with_a0);
+                };
                 if (two)
-                    ok = full ? chunk(std::true_type{}, std::true_type{}) : chunk(std::false_type{}, std::true_type{});
+                    ok = either(std::true_type{});
                 else if constexpr (!KV)
-                    ok = full ? chunk(std::true_type{}, std::false_type{}) : chunk(std::false_type{}, std::false_type{});
+                    ok = either(std::false_type{});
                 if (!ok) break;
             }
             if (!ok) break;

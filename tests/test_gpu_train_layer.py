@@ -346,3 +346,33 @@ def test_both_ways_through_the_binding_agree(fv, tr):  # noqa: F811
     got = tr.sparse_attn_lse(g, q, k, v, idx, cnt, scale=0.2, out=out, lse=lse, workspace=fv.attn_workspace(g))
     assert got[0] is out and got[1] is lse and torch.equal(bits(out), bits(a[0]))
     assert fv.get_status() == 0
+
+
+FEW_TILES = [
+    # few tiles, long lists: B, H, D, F, Hs, Ws, tf, th, tw, density, rows left empty, scale of Q
+    ("bs16-d64", (1, 1, 64, 4, 16, 48, 1, 4, 4), 0.6, (), 1.5),
+    ("bs16-d64-sparse", (1, 1, 64, 4, 16, 48, 1, 4, 4), 0.04, (1, 2), 1.5),
+    ("bs128-d128", (1, 1, 128, 4, 40, 38, 2, 8, 8), 0.8, (3,), 1.5),
+    ("bs32-d128-pad", (1, 2, 128, 3, 13, 21, 1, 4, 8), 0.9, (), 5.0),
+    ("bs64-d64-empty", (1, 1, 64, 3, 20, 41, 1, 8, 8), 0.5, (0, 2, 4), 5.0),
+    ("bs128-d64-all-kept", (2, 1, 64, 5, 23, 17, 2, 8, 8), 2.0, (), 1.0),
+]
+
+
+@pytest.mark.parametrize("name,geo,density,empty,qscale", FEW_TILES, ids=[x[0] for x in FEW_TILES])
+def test_few_tiles_with_long_lists_against_the_definition(fv, tr, name, geo, density, empty, qscale):  # noqa: F811
+    """Fewer tiles than SMs, lists of up to 24 chunks; a workspace full of NaN; the same bits twice."""
+    g = fv.geom(*geo)
+    idx, cnt = random_lists(g, density, 11, empty)
+    q, k, v, do = tiles(g, 12, (qscale, 1.0, 1.0, 1.0))
+    o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+    want, bound = definition(g, q, k, v, do, idx, cnt, 1 / math.sqrt(g.D))
+    outs = [torch.full_like(q, float("nan")) for _ in range(3)]
+    ws = tr.bwd_workspace(g).fill_(255)            # NaN in whatever is read before it is written
+    tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt, dq=outs[0], dk=outs[1], dv=outs[2], workspace=ws)
+    assert fv.get_status() == 0
+    for x, n in zip(outs, ("dq", "dk", "dv")):
+        check(x, want[n], bound[n], n)
+    again = tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt, workspace=ws)
+    for a, b in zip(outs, again):
+        assert torch.equal(bits(a), bits(b))
