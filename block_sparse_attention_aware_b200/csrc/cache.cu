@@ -4,9 +4,9 @@
 // Append moves every new key, value and query once: a bit copy of V and
 // (a, b) -> (a c - b s, a s + b c) on the pairs of K and Q, bound by memory.
 // One CTA a token, eight CTAs an SM: two frames of 1560 tokens with 40 query
-// and 40 key heads of 128 take 37.3 us, 5.2 TB/s read and written.  (Loads for
+// and 40 key heads of 128 take 35.8 us, 5.4 TB/s read and written.  (Loads for
 // four heads in flight a thread cost CTAs an SM, and 42 us; four tokens a CTA
-// likewise, 41 to 49.)  A single token is bound by the call, 13 us.
+// likewise, 41 to 49.)  A single token takes 2.5 us.
 //
 // Attention of one token reads each cached key and value once for a handful
 // of multiply-adds: bound by memory too, so the kernel's whole form follows
@@ -23,8 +23,8 @@
 // with mma.sync.m16n8k16 (8 heads an N tile; a tcgen05 tile would have 128
 // rows of which one to sixteen hold a query).  The parts' (maximum, sum, O)
 // are joined in part order by a second small kernel.  40 heads over 32760
-// tokens: 110 us, 6.1 TB/s; 24 ragged sequences up to 9000 tokens, 16-token
-// pages: 88 us, 5.3 TB/s (103 with a CTA for a third of the longest length).
+// tokens: 108 us, 6.2 TB/s; 24 ragged sequences up to 9000 tokens, 16-token
+// pages: 86 us, 5.5 TB/s (103 with a CTA for a third of the longest length).
 #include <cuda.h>
 
 #include <atomic>
@@ -621,15 +621,18 @@ static bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) 
 static bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // The split: parts of one size, so many tokens that the items fill the GPU's
-// CTA slots once, but no more than 512 (1024 where over four query heads share
-// a key head, whose partial results weigh more): several items a slot even
-// out ragged lengths, and the ring runs on from one to the next.  At least
-// 128 tokens, and at most DEC_MAX_PARTS parts.
+// CTA slots once, but no more than 512 (1024 where over eight query heads
+// share a key head, whose partial results weigh more): several items a slot
+// even out ragged lengths, and the ring runs on from one to the next.  With
+// 512 and 1024: 24 ragged sequences, 4 heads a key head 88.3 and 92.6 us; 48
+// sequences, 8 heads 47.6 and 51.2; 8 long ones, 16 heads 48.6 and 39.6; 40
+// heads over 32760 tokens alike.  (256: 88.9, and 123 for 110 in the last.)  At
+// least 128 tokens, and at most DEC_MAX_PARTS parts.
 static int split_parts(int B, int Hq, int Hkv, long long longest, int nsm, int* tokens) {
     const int group = Hq / Hkv;
     const long long base = static_cast<long long>(B) * Hkv * ((group + 15) / 16);
     const long long slots = static_cast<long long>(nsm) * DEC_CTAS;
-    const long long most = group > 4 ? 1024 : 512;
+    const long long most = group > 8 ? 1024 : 512;
     const double once = static_cast<double>(longest) * static_cast<double>(base) / static_cast<double>(slots);
     long long tk = once > static_cast<double>(most) ? most : static_cast<long long>(once);
     if (tk < 128) tk = 128;
