@@ -796,7 +796,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                         }
                     }
                     if (!ok) break;
-                    commit(&ctl.acc_full);
+                    // Two arrivals an item.  Without A0 both are warp 3's: warp 1, which has no part in the
+                    // accumulators then, may be an item of one chunk ahead, and its arrival for that one would
+                    // count for this.
+                    if (two || !first_role) commit(&ctl.acc_full);
+                    if (!two && !first_role) commit(&ctl.acc_full);
                     ++n_seq;
                 }
                 // every MMA this thread issued has completed before the tensor memory is released
