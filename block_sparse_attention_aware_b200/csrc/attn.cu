@@ -959,29 +959,17 @@ __global__ void __launch_bounds__(256) group_union_kernel(Geo g, int G, int ngro
         }
     }
     __syncwarp();
-    // lane l takes word 32r + l of round r; an exclusive scan of the words' union counts places them
+    // a word at a time, lane b its bit b (words to lanes left a short list's bits to one lane: 6 us for 32 blocks)
     uint32_t* dst = ulist + unit * nb;
     int base = 0;
-    for (int w0 = 0; w0 < nwords; w0 += 32) {
-        const int wd = w0 + lane;
-        uint32_t un = 0u;
-        if (wd < nwords)
-            for (int t = 0; t < G; ++t) un |= bits[t * nwords + wd];
-        const int c = __popc(un);
-        int incl = c;
+    for (int wd = 0; wd < nwords; ++wd) {
+        uint32_t mem = 0u;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        int k = base + incl - c;
-        for (uint32_t r = un; r != 0u; r &= r - 1u) {
-            const int b = __ffs(static_cast<int>(r)) - 1;
-            uint32_t mem = 0u;
-            for (int t = 0; t < G; ++t) mem |= ((bits[t * nwords + wd] >> b) & 1u) << t;
-            dst[k++] = static_cast<uint32_t>(wd * 32 + b) | (mem << 24);
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
+        for (int t = 0; t < MAX_GROUP; ++t)
+            if (t < G) mem |= ((bits[t * nwords + wd] >> lane) & 1u) << t;
+        const uint32_t any = __ballot_sync(0xffffffffu, mem != 0u);
+        if (mem) dst[base + __popc(any & ((1u << lane) - 1u))] = static_cast<uint32_t>(wd * 32 + lane) | (mem << 24);
+        base += __popc(any);
     }
     if (lane == 0) gcnt[unit] = base;
 }

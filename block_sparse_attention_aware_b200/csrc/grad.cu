@@ -927,29 +927,20 @@ __device__ __forceinline__ int grad_list(const Geo& g, int G, int nwords, const 
     if (!keys) {
         const int q0 = u * G, nq = min(G, g.nb - q0);
         for (int w0 = 0; w0 < nwords; w0 += 32) {
-            const int wd = w0 + lane;
-            uint32_t row[GRAD_GROUP], un = 0u;
+            uint32_t row[GRAD_GROUP];           // lane l has word w0 + l of the tile's rows
 #pragma unroll
-            for (int t = 0; t < GRAD_GROUP; ++t) {
-                row[t] = t < nq && wd < nwords ? __ldg(mat + static_cast<long long>(q0 + t) * nwords + wd) : 0u;
-                un |= row[t];
-            }
-            const int c = __popc(un);
-            int incl = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            int k = base + incl - c;
-            for (uint32_t r = un; r != 0u; r &= r - 1u) {
-                const int b = __ffs(static_cast<int>(r)) - 1;
+            for (int t = 0; t < GRAD_GROUP; ++t)
+                row[t] = t < nq && w0 + lane < nwords ? __ldg(mat + static_cast<long long>(q0 + t) * nwords + w0 + lane) : 0u;
+            for (int k = 0; k < min(32, nwords - w0); ++k) {   // a word at a time, lane b its bit b
                 uint32_t mem = 0u;
 #pragma unroll
-                for (int t = 0; t < GRAD_GROUP; ++t) mem |= ((row[t] >> b) & 1u) << t;
-                dst[k++] = static_cast<uint32_t>(wd * 32 + b) | (mem << 24);
+                for (int t = 0; t < GRAD_GROUP; ++t)
+                    if (t < G) mem |= ((__shfl_sync(0xffffffffu, row[t], k) >> lane) & 1u) << t;
+                const uint32_t any = __ballot_sync(0xffffffffu, mem != 0u);
+                if (mem)
+                    dst[base + __popc(any & ((1u << lane) - 1u))] = static_cast<uint32_t>((w0 + k) * 32 + lane) | (mem << 24);
+                base += __popc(any);
             }
-            base += __shfl_sync(0xffffffffu, incl, 31);
         }
     } else {
         const int wd = (u * G) >> 5, sh = (u * G) & 31;   // G divides 32: one word holds the tile's columns
