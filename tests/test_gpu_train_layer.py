@@ -348,20 +348,25 @@ def test_both_ways_through_the_binding_agree(fv, tr):  # noqa: F811
     assert fv.get_status() == 0
 
 
-FEW_TILES = [
+LONG = [
     # few tiles, long lists: B, H, D, F, Hs, Ws, tf, th, tw, density, rows left empty, scale of Q
-    ("bs16-d64", (1, 1, 64, 4, 16, 48, 1, 4, 4), 0.6, (), 1.5),
-    ("bs16-d64-sparse", (1, 1, 64, 4, 16, 48, 1, 4, 4), 0.04, (1, 2), 1.5),
+    ("bs16-d64", (1, 1, 64, 4, 16, 52, 1, 4, 4), 0.6, (), 1.5),
+    ("bs16-d64-sparse", (1, 1, 64, 4, 16, 52, 1, 4, 4), 0.04, (1, 2), 1.5),
     ("bs128-d128", (1, 1, 128, 4, 40, 38, 2, 8, 8), 0.8, (3,), 1.5),
     ("bs32-d128-pad", (1, 2, 128, 3, 13, 21, 1, 4, 8), 0.9, (), 5.0),
     ("bs64-d64-empty", (1, 1, 64, 3, 20, 41, 1, 8, 8), 0.5, (0, 2, 4), 5.0),
     ("bs128-d64-all-kept", (2, 1, 64, 5, 23, 17, 2, 8, 8), 2.0, (), 1.0),
+    # more tiles than SMs: some CTAs take a second one
+    ("left-bs16-d64", (1, 8, 64, 4, 16, 52, 1, 4, 4), 0.3, (1,), 1.5),
+    ("left-bs16-d128-sparse", (1, 7, 128, 4, 16, 50, 1, 4, 4), 0.02, (2, 4), 5.0),
+    ("left-bs128-d64", (2, 2, 64, 5, 24, 40, 2, 8, 8), 0.7, (3,), 4.0),
+    ("left-bs64-d128-pad", (1, 5, 128, 5, 23, 33, 1, 8, 8), 0.9, (), 0.5),
 ]
 
 
-@pytest.mark.parametrize("name,geo,density,empty,qscale", FEW_TILES, ids=[x[0] for x in FEW_TILES])
-def test_few_tiles_with_long_lists_against_the_definition(fv, tr, name, geo, density, empty, qscale):  # noqa: F811
-    """Fewer tiles than SMs, lists of up to 24 chunks; a workspace full of NaN; the same bits twice."""
+@pytest.mark.parametrize("name,geo,density,empty,qscale", LONG, ids=[x[0] for x in LONG])
+def test_long_lists_against_the_definition(fv, tr, name, geo, density, empty, qscale):  # noqa: F811
+    """Lists of tens of chunks; a workspace full of NaN; the same bits twice."""
     g = fv.geom(*geo)
     idx, cnt = random_lists(g, density, 11, empty)
     q, k, v, do = tiles(g, 12, (qscale, 1.0, 1.0, 1.0))
