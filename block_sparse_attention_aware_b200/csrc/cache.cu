@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
         if (tid == 0) {
             int ok = 0;
             long long row = -1;
-            if (b < a.B) {
+            if (b < a.B && (!a.cu || __ldg(a.cu + b) <= t)) {   // a row before the first sequence is none's
                 const int end = a.cu ? __ldg(a.cu + b + 1) : static_cast<int>(t) + 1;
                 const long long n = static_cast<long long>(__ldg(a.lens + b)) - (end - t);
                 int pg = -1;
@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
         const int e = tid - 32, i = e < D / 2 ? e : e - D / 2;
         int ax = 0;
         while (ax < a.axes - 1 && i >= a.pair_end[ax]) ++ax;
-        // rows behind the last sequence have no position to read
-        const bool live = t < (a.cu ? __ldg(a.cu + a.B) : a.B);
+        // rows outside the sequences have no position to read
+        const bool live = a.cu ? t >= __ldg(a.cu) && t < __ldg(a.cu + a.B) : t < a.B;
         const int n = live ? __ldg(a.pos + t * a.axes + ax) : 0;
         if (n >= 0 && n < a.rot_rows) {
             cs[e] = __ldg(a.rot + static_cast<long long>(n) * D + e);

@@ -50,7 +50,8 @@ typedef struct {
 /* Append new keys and values to the pages of B sequences.  Sequence b's new
  * tokens are rows cu[b] .. cu[b+1]-1 of k and v (cu NULL: row b alone), and
  * lens[b] is its length with them: its last new token is token lens[b] - 1.
- *   rows            rows of k, v, q; rows at and after cu[B] are left alone
+ *   rows            rows of k, v, q; rows before cu[0] and from cu[B] on are
+ *                   left alone (cu may be a slice of a larger batch's)
  *   k, v            [rows, Hkv, D] bf16, a row's heads contiguous, rows
  *                   k_stride and v_stride elements apart (multiples of 8)
  *   q, q_out        optional [rows, Hq, D] bf16 in and out, rows q_stride and

@@ -238,6 +238,33 @@ def test_shared_pages_strided_queries_and_another_stream(fv, ca):  # noqa: F811
     assert fv.get_status() == 0
 
 
+@pytest.mark.parametrize("rotated", [False, True])
+def test_rows_outside_the_sequences_are_left_alone(fv, ca, rotated):  # noqa: F811
+    """cu as a slice of a larger batch's: rows before its first entry and from its last one on belong to no sequence
+    here, whatever their positions hold."""
+    lens = [9, 20, 40]
+    c, table, ln = pool(ca, lens, 2, 64, 16, 5)
+    cu = torch.tensor([3, 5, 5, 8], dtype=I32, device="cuda")
+    q, k, v = (normal((11, h, 64), 30 + h) for h in (4, 2, 6))
+    v = v[:, :2]
+    kp, vp, qo = c.k_pages.clone(), c.v_pages.clone(), normal((11, 4, 64), 40)
+    want_q, args = qo.clone(), {}
+    if rotated:      # by nothing: cosines of 1, and positions outside the table in rows of no sequence
+        rot = torch.cat([torch.ones(4, 32), torch.zeros(4, 32)], 1).cuda()
+        pos = torch.full((11, 1), -7, dtype=I32, device="cuda")
+        pos[3:8] = 2
+        args = dict(pos=pos, rot=rot)
+    for b, (first, past) in enumerate([(3, 5), (5, 5), (5, 8)]):
+        for t in range(first, past):
+            n = lens[b] - past + t
+            page = int(table[b, n // 16])
+            kp[page, :, n % 16], vp[page, :, n % 16] = k[t], v[t]
+    want_q[3:8] = q[3:8]
+    assert c.append(k, v, table, ln, cu=cu, q=q, q_out=qo, **args) is qo
+    assert torch.equal(c.k_pages, kp) and torch.equal(c.v_pages, vp) and torch.equal(qo, want_q)
+    assert fv.get_status() == 0
+
+
 def test_nothing_to_append(fv, ca):  # noqa: F811
     c, table, ln = pool(ca, [10, 20], 2, 64, 16, 11)
     k0 = c.k_pages.clone()
