@@ -74,9 +74,11 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
         if (tid == 0) {
             int ok = 0;
             long long row = -1;
-            if (b < a.B && (!a.cu || __ldg(a.cu + b) <= t)) {   // a row before the first sequence is none's
-                const int end = a.cu ? __ldg(a.cu + b + 1) : static_cast<int>(t) + 1;
-                const long long n = static_cast<long long>(__ldg(a.lens + b)) - (end - t);
+            const int bb = min(b, a.B - 1);      // (the three loads together, whether the row has a sequence or not)
+            const long long first = a.cu ? __ldg(a.cu + bb) : t, end = a.cu ? __ldg(a.cu + bb + 1) : t + 1;
+            const int len = __ldg(a.lens + bb);
+            if (b < a.B && first <= t) {         // rows outside the sequences are none's
+                const long long n = len - (end - t);
                 int pg = -1;
                 if (n >= 0 && n < static_cast<long long>(a.width) * a.page)
                     pg = __ldg(a.table + static_cast<long long>(b) * a.width + n / a.page);
