@@ -170,7 +170,7 @@ __device__ __forceinline__ int block_extent(const Geo& g, int block) {
 __device__ __forceinline__ int chunk_block(const int32_t* list, int cl, int bpc, int nblk, int lane, int nb) {
     int j = 0;
     if (lane < nblk) {
-        j = __ldg(list + cl * bpc + lane);
+        j = list[cl * bpc + lane];
         if (j < 0 || j >= nb) {
             record_status(FVATTN_ERR_BOUNDS);
             j = 0;
@@ -185,7 +185,7 @@ __device__ __forceinline__ int chunk_block(const int32_t* list, int cl, int bpc,
 __device__ __forceinline__ int union_slot(const uint32_t* ul, int cl, int bpc, int nn, int lane, int nb,
                                           uint32_t& mem) {
     uint32_t e = 0u;
-    if (lane < nn) e = __ldg(ul + cl * bpc + lane);
+    if (lane < nn) e = ul[cl * bpc + lane];
     int j = static_cast<int>(e & 0xFFFFFFu);
     mem = e >> 24;
     if (lane < nn && j >= nb) {
@@ -629,12 +629,12 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                 const int units = GRP ? a.ngroups : g.nb;
                 const int hs = t / units;
                 const int r = t - hs * units;
-                const int bh = __ldg(a.head_order + hs);
-                const int u = __ldg(a.item_order + static_cast<long long>(bh) * units + r);
+                const int bh = a.head_order[hs];
+                const int u = a.item_order[static_cast<long long>(bh) * units + r];
                 const int qb = u * G;                     // first query block of the tile
                 const int nq = min(G, g.nb - qb);         // query blocks in the tile
-                int cnt = GRP ? __ldg(a.gcnt + static_cast<long long>(bh) * a.ngroups + u)
-                              : __ldg(a.kv_cnt + static_cast<long long>(bh) * g.nb + qb);
+                int cnt = GRP ? a.gcnt[static_cast<long long>(bh) * a.ngroups + u]
+                              : a.kv_cnt[static_cast<long long>(bh) * g.nb + qb];
                 constexpr int min_cnt = LSE ? 0 : 1;
                 if (cnt < min_cnt || cnt > g.nb) {
                     if (lane == 0) record_status(FVATTN_ERR_BOUNDS);
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                 } else {
                     j_next = chunk_block(list, 0, bpc, n_next, lane, g.nb);
                 }
-                int e_next = lane < n_next ? __ldg(a.ext + j_next) : 0;
+                int e_next = lane < n_next ? a.ext[j_next] : 0;
                 for (int cl = 0; cl < nc; ++cl, ++c_seq) {
                     const int stage = c_seq % KS;
                     const int nblk = n_next;
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                         } else {
                             j_next = chunk_block(list, cl + 1, bpc, n_next, lane, g.nb);
                         }
-                        e_next = lane < n_next ? __ldg(a.ext + j_next) : 0;
+                        e_next = lane < n_next ? a.ext[j_next] : 0;
                     }
                     if (!wait_warp(smem_u32(&ctl.k_empty[stage]), ((c_seq / KS) & 1) ^ 1, abort_flag, wlim)) {
                         ok = false;
@@ -919,8 +919,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
 // tile walks.  Order and repeats inside a list do not matter.  min_cnt: the
 // least list length that is in range.
 __global__ void __launch_bounds__(256) group_union_kernel(Geo g, int G, int ngroups, int nwords, int min_cnt,
-                                                          const int32_t* __restrict__ kv_idx,
-                                                          const int32_t* __restrict__ kv_cnt,
+                                                          const int32_t* kv_idx, const int32_t* kv_cnt,
                                                           uint32_t* __restrict__ ulist, int32_t* __restrict__ gcnt) {
     extern __shared__ uint32_t gb_smem[];   // [8 warps][G * nwords] membership bitmaps
     pdl_launch_dependents();
@@ -977,7 +976,7 @@ __global__ void __launch_bounds__(256) group_union_kernel(Geo g, int G, int ngro
 // One CTA per (b, h): order the head's `units` work units (query blocks, or
 // query groups when G > 1) by cost (kv blocks walked), longest first (ties by
 // lower index), and record the head's total cost.
-__global__ void __launch_bounds__(256) worklist_head_kernel(Geo g, int units, const int32_t* __restrict__ cost_in,
+__global__ void __launch_bounds__(256) worklist_head_kernel(Geo g, int units, const int32_t* cost_in,
                                                             int32_t* __restrict__ item_order,
                                                             long long* __restrict__ head_cost) {
     extern __shared__ int wl_hist[];   // [nb + 2]
@@ -1022,7 +1021,7 @@ __global__ void __launch_bounds__(256) worklist_head_kernel(Geo g, int units, co
 
 // Single CTA: heads by total cost, heaviest first (ties by lower index);
 // resets the item counter; writes every block's real extent.
-__global__ void __launch_bounds__(256) worklist_heads_kernel(Geo g, int BH, const long long* __restrict__ head_cost,
+__global__ void __launch_bounds__(256) worklist_heads_kernel(Geo g, int BH, const long long* head_cost,
                                                              int32_t* __restrict__ head_order, int* counter,
                                                              int32_t* __restrict__ ext) {
     pdl_launch_dependents();

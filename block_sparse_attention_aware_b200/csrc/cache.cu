@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
         // the token's sequence: how many sequences end at or before it
         int b = 0;
         if (a.cu) {
-            for (int i = tid; i < a.B; i += 32) b += __ldg(a.cu + i + 1) <= t;
+            for (int i = tid; i < a.B; i += 32) b += a.cu[i + 1] <= t;
             b = __reduce_add_sync(0xffffffffu, b);
         } else {
             b = t < a.B ? static_cast<int>(t) : a.B;
@@ -75,13 +75,13 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
             int ok = 0;
             long long row = -1;
             const int bb = min(b, a.B - 1);      // (the three loads together, whether the row has a sequence or not)
-            const long long first = a.cu ? __ldg(a.cu + bb) : t, end = a.cu ? __ldg(a.cu + bb + 1) : t + 1;
-            const int len = __ldg(a.lens + bb);
+            const long long first = a.cu ? a.cu[bb] : t, end = a.cu ? a.cu[bb + 1] : t + 1;
+            const int len = a.lens[bb];
             if (b < a.B && first <= t) {         // rows outside the sequences are none's
                 const long long n = len - (end - t);
                 int pg = -1;
                 if (n >= 0 && n < static_cast<long long>(a.width) * a.page)
-                    pg = __ldg(a.table + static_cast<long long>(b) * a.width + n / a.page);
+                    pg = a.table[static_cast<long long>(b) * a.width + n / a.page];
                 if (pg >= 0 && pg < a.pages) {
                     row = (static_cast<long long>(pg) * a.Hkv * a.page + n % a.page) * D;
                     ok = 1;
@@ -98,10 +98,10 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
         int ax = 0;
         while (ax < a.axes - 1 && i >= a.pair_end[ax]) ++ax;
         // rows outside the sequences have no position to read
-        const bool live = a.cu ? t >= __ldg(a.cu) && t < __ldg(a.cu + a.B) : t < a.B;
-        const int n = live ? __ldg(a.pos + t * a.axes + ax) : 0;
+        const bool live = a.cu ? t >= a.cu[0] && t < a.cu[a.B] : t < a.B;
+        const int n = live ? a.pos[t * a.axes + ax] : 0;
         if (n >= 0 && n < a.rot_rows) {
-            cs[e] = __ldg(a.rot + static_cast<long long>(n) * D + e);
+            cs[e] = a.rot[static_cast<long long>(n) * D + e];
         } else {
             record_status(FVATTN_ERR_BOUNDS);
             bad = true;
@@ -216,7 +216,7 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 
 // A sequence's length, range-checked.
 __device__ __forceinline__ int cache_len(const DecArgs& a, int b) {
-    const int n = __ldg(a.lens + b);
+    const int n = a.lens[b];
     const long long cap = min(a.longest, static_cast<long long>(a.width) * a.page);
     if (n < 0 || n > cap) {
         record_status(FVATTN_ERR_BOUNDS);
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DEC_CTAS)
             // a lane's page of the tile at t; looked up a tile ahead of its use
             auto page_of = [&](int t) {
                 const int tok = t + lane * box;
-                return lane < boxes && tok < t1 ? __ldg(row + tok / a.page) : 0;
+                return lane < boxes && tok < t1 ? row[tok / a.page] : 0;
             };
             int next = page_of(t0);
             for (int t = t0; t < t1; t += DEC_TILE, ++it) {
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DEC_CTAS)
             for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    qf[n][kk][i] = h < nheads ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + i * 8 + 2 * tq)) : 0u;
+                    qf[n][kk][i] = h < nheads ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + i * 8 + 2 * tq) : 0u;
         }
         const uint32_t tiles = static_cast<uint32_t>((t1 - t0 + DEC_TILE - 1) / DEC_TILE);
         for (uint32_t i = (it ^ static_cast<uint32_t>(warp >> 1)) & 1u; i < tiles; i += 2) {

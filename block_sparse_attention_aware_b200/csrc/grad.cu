@@ -158,7 +158,7 @@ __device__ __forceinline__ int grad_extent(const Geo& g, int block) {
 __device__ __forceinline__ int grad_slot(const uint32_t* ul, int e, int cnt, uint32_t& mem) {
     mem = 0u;
     if (e >= cnt) return -1;
-    const uint32_t v = __ldg(ul + e);
+    const uint32_t v = ul[e];
     mem = v >> 24;
     return static_cast<int>(v & 0xFFFFFFu);
 }
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 int f_, y_, x_;
                 live = live && token_of_pos(g, static_cast<long long>(blk0) * bs + row, f_, y_, x_);
             } else {
-                const float nl = in_tile ? __ldg(a.nlse2 + grow) : -INFINITY;
+                const float nl = in_tile ? a.nlse2[grow] : -INFINITY;
                 if (in_tile) nd = a.ndelta[grow];
                 live = nl != -INFINITY;
                 nl2 = f2_pack(nl, nl);
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                     break;
                 }
                 const int bh = t / a.ngroups;
-                const int entry = __ldg(a.order + t);
+                const int entry = a.order[t];
                 const int u = entry & 0xFFF, cnt = (entry >> 12) & 0xFFF;
                 const long long unit = static_cast<long long>(bh) * a.ngroups + u;
                 if (lane == 0) {
@@ -567,14 +567,14 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
                 // a chunk's blocks, membership bits and real extents are looked up a chunk ahead
                 uint32_t m_next = 0u;
                 int j_next = lane < bpc ? grad_slot(ul, lane, cnt, m_next) : -1;
-                int e_next = !KV && j_next >= 0 ? __ldg(a.ext + j_next) : 0;
+                int e_next = !KV && j_next >= 0 ? a.ext[j_next] : 0;
                 for (int i = 0; i < nc; ++i, ++c) {
                     const int st = c % NS0;
                     const uint32_t mem = m_next;
                     const int j = j_next, ext = e_next;
                     if (i + 1 < nc) {
                         j_next = lane < bpc ? grad_slot(ul, (i + 1) * bpc + lane, cnt, m_next) : -1;
-                        e_next = !KV && j_next >= 0 ? __ldg(a.ext + j_next) : 0;
+                        e_next = !KV && j_next >= 0 ? a.ext[j_next] : 0;
                     }
                     if (!wait_warp(smem_u32(&ctl.b0_empty[st]), ((c / NS0) & 1) ^ 1, abort_flag, wlim)) {
                         ok = false;
@@ -827,11 +827,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
 // head write the blocks' extents.
 template <int D>
 __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, int nwords,
-                                                        const uint4* __restrict__ o, const uint4* __restrict__ dout,
-                                                        const uint4* __restrict__ v,
-                                                        const float* __restrict__ lse,
-                                                        const int32_t* __restrict__ kv_idx,
-                                                        const int32_t* __restrict__ kv_cnt,
+                                                        const uint4* o, const uint4* dout, const uint4* v,
+                                                        const float* lse, const int32_t* kv_idx, const int32_t* kv_cnt,
                                                         float* __restrict__ nlse2, float* __restrict__ ndelta,
                                                         float2* __restrict__ norms, uint32_t* __restrict__ bits,
                                                         int32_t* __restrict__ ext) {
@@ -849,9 +846,9 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, 
 #pragma unroll
         for (int i = 0; i < 8 / RPI; ++i) {
             const long long at = (row0 + i * RPI) * LPR + lane;
-            x[i] = __ldg(o + at);
-            y[i] = __ldg(dout + at);
-            z[i] = __ldg(v + at);
+            x[i] = o[at];
+            y[i] = dout[at];
+            z[i] = v[at];
         }
         float o2max = 0.f, v2 = 0.f;
 #pragma unroll
@@ -897,14 +894,14 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, 
     uint32_t* mine = gp_bits + warp * nwords;
     for (int i = lane; i < nwords; i += 32) mine[i] = 0u;
     __syncwarp();
-    int cnt = __ldg(kv_cnt + unit);
+    int cnt = kv_cnt[unit];
     if (cnt < 0 || cnt > g.nb) {
         if (lane == 0) record_status(FVATTN_ERR_BOUNDS);
         cnt = cnt < 0 ? 0 : g.nb;
     }
     const int32_t* list = kv_idx + unit * g.nb;
     for (int e = lane; e < cnt; e += 32) {
-        const int j = __ldg(list + e);
+        const int j = list[e];
         if (j < 0 || j >= g.nb) {
             record_status(FVATTN_ERR_BOUNDS);
             continue;
@@ -920,7 +917,7 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, 
 // list's length.  Direction 0: a query tile u and key blocks, from the rows of
 // the bit matrix; 1 (keys): a key tile and query blocks, from its columns.
 // One warp.
-__device__ __forceinline__ int grad_list(const Geo& g, int G, int nwords, const uint32_t* __restrict__ mat, bool keys,
+__device__ __forceinline__ int grad_list(const Geo& g, int G, int nwords, const uint32_t* mat, bool keys,
                                          int u, uint32_t* __restrict__ dst) {
     const int lane = threadIdx.x & 31;
     int base = 0;
@@ -930,7 +927,7 @@ __device__ __forceinline__ int grad_list(const Geo& g, int G, int nwords, const 
             uint32_t row[GRAD_GROUP];           // lane l has word w0 + l of the tile's rows
 #pragma unroll
             for (int t = 0; t < GRAD_GROUP; ++t)
-                row[t] = t < nq && w0 + lane < nwords ? __ldg(mat + static_cast<long long>(q0 + t) * nwords + w0 + lane) : 0u;
+                row[t] = t < nq && w0 + lane < nwords ? mat[static_cast<long long>(q0 + t) * nwords + w0 + lane] : 0u;
             for (int k = 0; k < min(32, nwords - w0); ++k) {   // a word at a time, lane b its bit b
                 uint32_t mem = 0u;
 #pragma unroll
@@ -947,7 +944,7 @@ __device__ __forceinline__ int grad_list(const Geo& g, int G, int nwords, const 
         const uint32_t ones = (1u << G) - 1u;
         for (int i0 = 0; i0 < g.nb; i0 += 32) {
             const int i = i0 + lane;
-            const uint32_t mem = i < g.nb ? (__ldg(mat + static_cast<long long>(i) * nwords + wd) >> sh) & ones : 0u;
+            const uint32_t mem = i < g.nb ? (mat[static_cast<long long>(i) * nwords + wd] >> sh) & ones : 0u;
             const uint32_t any = __ballot_sync(0xffffffffu, mem != 0u);
             if (mem) dst[base + __popc(any & ((1u << lane) - 1u))] = static_cast<uint32_t>(i) | (mem << 24);
             base += __popc(any);
@@ -963,8 +960,7 @@ __device__ __forceinline__ int grad_list(const Geo& g, int G, int nwords, const 
 constexpr int LISTS_THREADS = 1024;
 
 __global__ void __launch_bounds__(LISTS_THREADS) grad_lists_kernel(Geo g, int G, int ngroups, int nwords,
-                                                                   const uint32_t* __restrict__ bits,
-                                                                   const float2* __restrict__ norms,
+                                                                   const uint32_t* bits, const float2* norms,
                                                                    uint32_t* __restrict__ ulq, uint32_t* __restrict__ ulk,
                                                                    int32_t* __restrict__ ordq, int32_t* __restrict__ ordk,
                                                                    int* __restrict__ counters) {

@@ -629,7 +629,7 @@ __device__ unsigned long long sel_boundary(const float (&v)[NPL], const float (&
 // order, m = min(nb, max(m_p, min(k, nb)) + kextra), m_p the Top-p crossing
 // (first prefix whose mass reaches p * total; 0 when p = 0, nb when p >= 1).
 template <int NPL, bool KEEP_E>
-__global__ void __launch_bounds__(32 * SEL_WARPS, NPL <= 24 ? 4 : 1) select_kernel(int nb, long long rows, const float* __restrict__ L,
+__global__ void __launch_bounds__(32 * SEL_WARPS, NPL <= 24 ? 4 : 1) select_kernel(int nb, long long rows, const float* L,
                                                                 double p, int kfloor, int kextra,
                                                                 int32_t* __restrict__ kv_idx,
                                                                 int32_t* __restrict__ kv_cnt) {

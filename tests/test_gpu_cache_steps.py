@@ -382,3 +382,42 @@ def test_capture_behind_copies_fills_and_another_stream(fv, ca):  # noqa: F811
         assert torch.equal(a, b)
     assert torch.equal(sums[0], c.k_pages.sum()) and torch.equal(sums[1], o.float().sum())
     assert fv.get_status() == 0
+
+
+@pytest.mark.parametrize("longest", [60, 900])
+def test_steps_without_a_sync_between_them(fv, ca, longest):  # noqa: F811
+    """Append and attention in turn, hundreds of them in flight, with one buffer for the rotated queries, one for the
+    lengths and one workspace: every step reads what the one before it left there, not what an earlier one did."""
+    hq, hkv, D, page, B, steps = 8, 2, 64, 16, 3, 300
+    c, table, _ = pool(ca, [longest] * B, hkv, D, page, 3)
+    k0, v0 = c.k_pages.clone(), c.v_pages.clone()
+    rot = ca.rotation_table(D, (D // 2,), 1000)
+    ks, vs = normal((steps, B, hkv, D), 1), normal((steps, B, hkv, D), 2)
+    qs = normal((steps, B, hq, D), 3, 2.0)
+    gen = torch.Generator().manual_seed(4)
+    lens = torch.randint(1, longest + 1, (steps, B), generator=gen, dtype=I32).cuda()
+    pos = torch.randint(0, 1000, (steps, B, 1), generator=gen, dtype=I32).cuda()
+    q = torch.zeros((B, hq, D), dtype=BF16, device="cuda")
+    ws = c.attend_workspace(B, hq, longest)
+
+    def run(sync):
+        c.k_pages.copy_(k0)
+        c.v_pages.copy_(v0)
+        o = torch.zeros((steps, B, hq, D), dtype=BF16, device="cuda")
+        lse = torch.zeros((steps, B, hq), device="cuda")
+        torch.cuda.synchronize()
+        for i in range(steps):
+            c.append(ks[i], vs[i], table, lens[i], q=qs[i], q_out=q, pos=pos[i], rot=rot)
+            if sync:
+                torch.cuda.synchronize()
+            c.attend(q, table, lens[i], longest=longest, out=o[i], lse=lse[i], workspace=ws)
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return o, lse, c.k_pages.clone(), c.v_pages.clone()
+
+    want = run(True)
+    for _ in range(3):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
+    assert fv.get_status() == 0

@@ -401,3 +401,31 @@ def test_many_tiles_with_lists_of_a_chunk_or_two(fv, tr, D, keep):  # noqa: F811
         for a, b in zip(first, tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt)):
             assert torch.equal(bits(a), bits(b))
     assert fv.get_status() == 0
+
+
+@pytest.mark.parametrize("geo", [(1, 2, 64, 2, 8, 8, 2, 2, 4), GEO64, GEO], ids=["bs16", "bs64", "bs128"])
+def test_calls_without_a_sync_between_them(fv, tr, geo):  # noqa: F811
+    """Forward and backward passes of two sets of inputs in turn, many in flight, with one workspace for each
+    operator: a call reads its own lists, orders and statistics there, not those of the call before."""
+    g = fv.geom(*geo)
+    sets = []
+    for s in range(2):
+        idx, cnt = random_lists(g, 0.3 + 0.5 * s, 40 + s, (s,))
+        sets.append((*tiles(g, 50 + s, (1.0 + 3 * s, 1.0, 1.0, 1.0)), idx, cnt))
+    aw, bw = fv.attn_workspace(g), tr.bwd_workspace(g)
+
+    def step(q, k, v, do, idx, cnt):
+        o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt, workspace=aw)
+        return (o, lse, *tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt, workspace=bw))
+
+    want = []
+    for s in sets:
+        torch.cuda.synchronize()
+        want.append(step(*s))
+        torch.cuda.synchronize()
+    got = [step(*sets[i % 2]) for i in range(60)]
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        for a, b in zip(outs, want[i % 2]):
+            assert torch.equal(a, b)
+    assert fv.get_status() == 0

@@ -212,3 +212,26 @@ def test_the_extension_leaves_all_but_the_plain_case_to_the_bindings(mods):
         assert f() is NotImplemented and f(*[None] * count) is NotImplemented and f(*[1] * count) is NotImplemented
         assert f(*[t] * count) is NotImplemented                       # not on a GPU
         assert f(g, *[t] * (count - 1)) is NotImplemented
+
+
+# ------------------------------------------------------------------ sources
+
+CSRC = os.path.join(ROOT, "block_sparse_attention_aware_b200", "csrc")
+
+
+def _code(name):
+    src = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", re.sub(r"/\*.*?\*/", "", src, flags=re.S))
+
+
+@pytest.mark.parametrize("name", ["attn.cu", "cache.cu", "grad.cu", "route.cu", "common.cuh", "ptx.cuh"])
+def test_kernels_that_start_early_read_with_plain_loads(name):
+    """A kernel that waits for the one before it after its own start (pdl_wait) may have begun while its inputs were
+    written: nothing in it goes through the read-only path, which takes inputs as constant from the kernel's start."""
+    src = _code(name)
+    if name == "route.cu":       # some of its kernels start after all before them have ended
+        parts = [p for p in src.split("__global__")[1:] if "pdl_wait()" in p]
+        assert len(parts) == 2
+        src = "\n".join(parts)
+    for path in (r"__ldg\s*\(", r"ld\.global\.nc", r"const\s+[\w:]+\s*\*\s*__restrict__"):
+        assert not re.search(path, src), path
