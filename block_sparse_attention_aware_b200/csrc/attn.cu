@@ -106,6 +106,7 @@ struct AttnArgs {
     unsigned long long* sm_stats;
     float scale_log2;            // scale * log2(e), > 0
     int total_items;
+    int oob_row;                 // a row index past the end of every operand (reads as zero)
     unsigned long long wait_limit_ns;   // bound of every wait (fault-injection tests shorten it)
     int hooks;                   // FVATTN_HOOK_* fault injection (0 in normal use)
 };
@@ -789,12 +790,15 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                         break;
                     }
                     const uint32_t bar = smem_u32(&ctl.v_full[stage]);
-                    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(nblk * bs * D * 2));
+                    if (lane == 0) mbar_arrive_expect_tx(bar, L::KV_BYTES);
                     __syncwarp();
-                    if (lane < nblk) {
+                    if (lane < bpc) {
+                        // a slot without a block is filled with zeros (a row past the end): P is 0 there, and 0
+                        // times what an earlier item left could be NaN
+                        const int r = lane < nblk ? row_base + j * bs : a.oob_row;
                         const uint32_t vb = sV + stage * L::KV_BYTES + lane * bs * 128u;
 #pragma unroll
-                        for (int h = 0; h < D / 64; ++h) tma_load_2d(vb + h * 16384u, &tmV, h * 64, row_base + j * bs, bar);
+                        for (int h = 0; h < D / 64; ++h) tma_load_2d(vb + h * 16384u, &tmV, h * 64, r, bar);
                     }
                 }
                 ++item_seq;
@@ -1197,6 +1201,7 @@ static int attn_impl(const fvattn_geom* gp, const void* q_t, const void* k_t, co
     args.gcnt = gcnt;
     args.ext = ext;
     args.total_items = BH * units;
+    args.oob_row = static_cast<int>(rows);
     const unsigned long long hook_limit = g_hook_wait_limit_ns.load();
     args.wait_limit_ns = hook_limit ? hook_limit : WAIT_LIMIT_NS;
     args.hooks = g_hook_flags.load();

@@ -421,3 +421,26 @@ def test_steps_without_a_sync_between_them(fv, ca, longest):  # noqa: F811
         for a, b in zip(run(False), want):
             assert torch.equal(a, b)
     assert fv.get_status() == 0
+
+
+@pytest.mark.parametrize("stream", [False, True], ids=["extension", "bindings"])
+def test_rows_that_take_no_part_are_zero_in_queries_made_by_the_call(fv, ca, stream):  # noqa: F811
+    """Rows outside the sequences and refused tokens: zero where the call makes q_out, left alone where it is given."""
+    c, table, ln = pool(ca, [40, 7], 2, 64, 16, 3)
+    rows, hq, D = 9, 4, 64
+    k, v, q = normal((rows, 2, D), 1), normal((rows, 2, D), 2), normal((rows, hq, D), 3)
+    cu = torch.tensor([2, 4, 7], dtype=I32, device="cuda")
+    rot = ca.rotation_table(D, (32,), 100)
+    pos = torch.arange(rows, dtype=I32, device="cuda").view(-1, 1)
+    pos[5] = 100                                            # past the table: refused
+    kw = dict(cu=cu, q=q, pos=pos, rot=rot, stream=torch.cuda.current_stream() if stream else None)
+    out = torch.full_like(q, 7.0)
+    assert c.append(k, v, table, ln, q_out=out, **kw) is out
+    assert fv.get_status() == fv.ERR_BOUNDS
+    junk = [torch.full_like(q, float("nan")) for _ in range(8)]      # what a fresh block of this size may hold
+    del junk
+    got = c.append(k, v, table, ln, **kw)
+    assert fv.get_status() == fv.ERR_BOUNDS
+    part = torch.tensor([i in (2, 3, 4, 6) for i in range(rows)], device="cuda")
+    assert torch.equal(bits(got[part]), bits(out[part]))
+    assert (got[~part] == 0).all() and (out[~part] == 7.0).all()

@@ -429,3 +429,34 @@ def test_calls_without_a_sync_between_them(fv, tr, geo):  # noqa: F811
         for a, b in zip(outs, want[i % 2]):
             assert torch.equal(a, b)
     assert fv.get_status() == 0
+
+
+@pytest.mark.parametrize("geo", [(2, 8, 64, 4, 16, 52, 1, 4, 4), (2, 12, 128, 4, 16, 48, 2, 4, 4), (2, 8, 64, 4, 40, 48, 1, 8, 8)],
+                         ids=["bs16", "bs32", "bs64"])
+def test_nan_stays_in_its_head(fv, tr, geo):  # noqa: F811
+    """NaN in Q, K and V of some heads, more tiles than SMs, the other heads' lists filling half a chunk of
+    128 keys: what a CTA's buffers keep of those heads reaches no other head's results, in no bit."""
+    g = fv.geom(*geo)
+    tile = 128 // g.bs
+    idx = torch.zeros((g.B, g.H, g.nb, g.nb), dtype=torch.int32)
+    gen = torch.Generator().manual_seed(21)
+    idx[..., 0] = (torch.arange(g.nb) // tile * 5 + torch.randint(0, tile // 2, (g.B, g.H, g.nb), generator=gen)) % g.nb
+    cnt = torch.ones((g.B, g.H, g.nb), dtype=torch.int32)
+    cnt[:, :3], idx[:, :3, :, :tile] = tile, torch.arange(tile, dtype=torch.int32)
+    idx, cnt = idx.cuda(), cnt.cuda()
+    q, k, v, do = tiles(g, 22)
+
+    def run():
+        o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+        inference = fv.sparse_attn(g, q, k, v, idx, cnt)
+        raster_o = fv.sparse_attn_raster(g, q, k, v, idx, cnt)
+        return (o, lse[..., None], inference, raster_o.transpose(1, 2), *tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt))
+
+    want = run()
+    for i in range(3):
+        for t in (q, k, v)[i:]:
+            t[:, i] = float("nan")
+    for _ in range(3):
+        for a, b in zip(run(), want):
+            assert torch.equal(a[:, 3:], b[:, 3:])
+    assert fv.get_status() == 0
