@@ -21,10 +21,15 @@
 // on the way, which the key pass reads.  Its own dQ is put right at the end,
 //   dQ = scale (sum_u dS0_tu k_u - (delta - delta0) sum_u P_tu k_u),
 // with a product more, in the tiles that need it.  delta0's error is about
-// 2^-9 |dO| |O| / sqrt(3 D) and dP - delta varies by |dO| |v| / sqrt(D), so
-// that it adds |O| / |v| roundings to the result: tiles with a row of
-// |O|^2 > GRAD_EXACT mean |v|^2 take the product (1/16: an error of at most
-// sqrt(2 + 1/16) = 1.44 roundings in the others).
+// 2^-9 |dO| |O| / sqrt(3 D) and dP_tu - delta_t = dO_t . (v_u - O_t) about
+// |dO| |v_u - O| / sqrt(D), so that it adds |O| / min_u |v_u - O| roundings to
+// the result at most.  Tiles with a row of |O|^2 > GRAD_EXACT min |v_u|^2, u
+// the tokens of the tile's listed blocks, take the product.  With 1/16,
+// |v_u - O| >= 3 |O| in the others, and their error is at most
+// sqrt(2 + 1/9) = 1.45 roundings.  (The head's mean |v|^2 in the minimum's
+// place let a few large values, even of blocks that no list holds, turn the
+// product off where the softmax was concentrated: 2.3 to 3.1 roundings a row at
+// scores of standard deviation 3.)
 //
 // Both passes are one kernel, grad_kernel<D, KV>, one CTA of 640 threads per
 // SM (it holds all 512 tensor-memory columns):
@@ -822,7 +827,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
 // First `stat_blocks` CTAs: -lse * log2(e) and -dO . O of every row (one warp
 // per 8 rows; 16 bytes of O and dO a lane), the former -inf for padding rows
 // and rows that keep no block, so that their P is 0; and for each 8 rows the
-// largest |O|^2 and the sum of |v|^2.  The others: one warp
+// largest |O|^2 and the least |v|^2 of a token (inf without one).  The others: one warp
 // per (b, h, query block) writes its kv list as a bit row; those of the first
 // head write the blocks' extents.
 template <int D>
@@ -850,12 +855,15 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, 
             y[i] = dout[at];
             z[i] = v[at];
         }
-        float o2max = 0.f, v2 = 0.f;
+        int f_, y_, x_;
+        const bool token = lane < 8 && token_of_pos(g, (row0 + lane) % g.Npad, f_, y_, x_);
+        const uint32_t tokens = __ballot_sync(0xffffffffu, token);
+        float o2max = 0.f, v2min = INFINITY;
 #pragma unroll
         for (int i = 0; i < 8 / RPI; ++i) {
             const uint32_t xa[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ya[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
             const uint32_t za[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
-            float s = 0.f, o2 = 0.f;
+            float s = 0.f, o2 = 0.f, v2 = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float x0 = __uint_as_float(xa[k] << 16), x1 = __uint_as_float(xa[k] & 0xFFFF0000u);
@@ -869,22 +877,22 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, 
             for (int d = LPR / 2; d > 0; d >>= 1) {
                 s += __shfl_xor_sync(0xffffffffu, s, d);
                 o2 += __shfl_xor_sync(0xffffffffu, o2, d);
+                v2 += __shfl_xor_sync(0xffffffffu, v2, d);
             }
             o2max = fmaxf(o2max, o2);
+            if ((tokens >> (i * RPI + lane / LPR)) & 1u) v2min = fminf(v2min, v2);
             if (lane % LPR == 0) ndelta[row0 + i * RPI + lane / LPR] = -s;
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
             o2max = fmaxf(o2max, __shfl_xor_sync(0xffffffffu, o2max, d));
-            v2 += __shfl_xor_sync(0xffffffffu, v2, d);
+            v2min = fminf(v2min, __shfl_xor_sync(0xffffffffu, v2min, d));
         }
-        if (lane == 0) norms[row0 / 8] = make_float2(o2max, v2);
+        if (lane == 0) norms[row0 / 8] = make_float2(o2max, v2min);
         if (lane < 8) {
             const long long r = row0 + lane;
-            int f_, y_, x_;
             const float l = lse[r];
-            const bool takes_part = token_of_pos(g, r % g.Npad, f_, y_, x_) && l != -INFINITY;
-            nlse2[r] = takes_part ? -l * 1.4426950408889634f : -INFINITY;
+            nlse2[r] = token && l != -INFINITY ? -l * 1.4426950408889634f : -INFINITY;
         }
         return;
     }
@@ -915,12 +923,13 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(Geo g, int stat_blocks, 
 // The blocks that a tile of G blocks is paired with, ascending, each with its
 // membership bits above bit 24 (bit t: paired with the tile's block t); the
 // list's length.  Direction 0: a query tile u and key blocks, from the rows of
-// the bit matrix; 1 (keys): a key tile and query blocks, from its columns.
-// One warp.
+// the bit matrix, with `least` the least of the listed blocks' vmin; 1 (keys):
+// a key tile and query blocks, from its columns.  One warp.
 __device__ __forceinline__ int grad_list(const Geo& g, int G, int nwords, const uint32_t* mat, bool keys,
-                                         int u, uint32_t* __restrict__ dst) {
+                                         int u, const float* vmin, float& least, uint32_t* __restrict__ dst) {
     const int lane = threadIdx.x & 31;
     int base = 0;
+    least = INFINITY;
     if (!keys) {
         const int q0 = u * G, nq = min(G, g.nb - q0);
         for (int w0 = 0; w0 < nwords; w0 += 32) {
@@ -934,11 +943,16 @@ __device__ __forceinline__ int grad_list(const Geo& g, int G, int nwords, const 
                 for (int t = 0; t < GRAD_GROUP; ++t)
                     if (t < G) mem |= ((__shfl_sync(0xffffffffu, row[t], k) >> lane) & 1u) << t;
                 const uint32_t any = __ballot_sync(0xffffffffu, mem != 0u);
-                if (mem)
-                    dst[base + __popc(any & ((1u << lane) - 1u))] = static_cast<uint32_t>((w0 + k) * 32 + lane) | (mem << 24);
+                if (mem) {
+                    const int j = (w0 + k) * 32 + lane;
+                    dst[base + __popc(any & ((1u << lane) - 1u))] = static_cast<uint32_t>(j) | (mem << 24);
+                    least = fminf(least, vmin[j]);
+                }
                 base += __popc(any);
             }
         }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, d));
     } else {
         const int wd = (u * G) >> 5, sh = (u * G) & 31;   // G divides 32: one word holds the tile's columns
         const uint32_t ones = (1u << G) - 1u;
@@ -965,37 +979,42 @@ __global__ void __launch_bounds__(LISTS_THREADS) grad_lists_kernel(Geo g, int G,
                                                                    int32_t* __restrict__ ordq, int32_t* __restrict__ ordk,
                                                                    int* __restrict__ counters) {
     const int BH = g.B * g.H, nb = g.nb;
-    __shared__ float part[LISTS_THREADS];
-    extern __shared__ int go_start[];   // [nb + 1], then the tiles' list lengths [ngroups]
+    extern __shared__ int go_start[];   // [nb + 1], then by tile [ngroups] the lists' lengths, by block [nb] and by
+                                        // tile [ngroups] the least |v|^2 and the largest |O|^2
     int* cnt = go_start + nb + 1;
+    float* vmin = reinterpret_cast<float*>(cnt + ngroups);
+    float* omax = vmin + nb;
     pdl_launch_dependents();
     pdl_wait();
     const int dir = static_cast<int>(blockIdx.x) / BH, bh = static_cast<int>(blockIdx.x) - dir * BH;
     const long long unit0 = static_cast<long long>(bh) * ngroups;
     int32_t* ord = (dir ? ordk : ordq) + unit0;
-    for (int u = threadIdx.x >> 5; u < ngroups; u += LISTS_THREADS / 32) {
-        const int n = grad_list(g, G, nwords, bits + static_cast<long long>(bh) * nb * nwords, dir != 0, u,
-                                (dir ? ulk : ulq) + (unit0 + u) * nb);
-        if ((threadIdx.x & 31) == 0) cnt[u] = n;
-    }
     if (bh == 0 && threadIdx.x == 0) counters[dir] = 0;
-    const int n8 = static_cast<int>(g.Npad / 8);
-    norms += static_cast<long long>(bh) * n8;
-    float limit = 0.f;
     if (dir == 0) {
-        float v2 = 0.f;
-        for (int i = threadIdx.x; i < n8; i += LISTS_THREADS) v2 += norms[i].y;
-        part[threadIdx.x] = v2;
-        __syncthreads();
-        for (int d = LISTS_THREADS / 2; d > 0; d >>= 1) {
-            if (static_cast<int>(threadIdx.x) < d) part[threadIdx.x] += part[threadIdx.x + d];
-            __syncthreads();
+        norms += static_cast<long long>(bh) * (g.Npad / 8);
+        const int n = g.bs / 8;
+        for (int i = threadIdx.x; i < nb; i += LISTS_THREADS) {
+            float x = INFINITY;
+            for (int k = 0; k < n; ++k) x = fminf(x, norms[i * n + k].y);
+            vmin[i] = x;
         }
-        limit = GRAD_EXACT * part[0] / static_cast<float>(g.N);
+        for (int i = threadIdx.x; i < ngroups; i += LISTS_THREADS) {
+            float x = 0.f;
+            for (int k = i * G * n; k < min(i * G + G, nb) * n; ++k) x = fmaxf(x, norms[k].x);
+            omax[i] = x;
+        }
+        __syncthreads();
+    }
+    for (int u = threadIdx.x >> 5; u < ngroups; u += LISTS_THREADS / 32) {
+        float least;
+        const int n = grad_list(g, G, nwords, bits + static_cast<long long>(bh) * nb * nwords, dir != 0, u, vmin, least,
+                                (dir ? ulk : ulq) + (unit0 + u) * nb);
+        // (in a list's length: whether its tile needs the exact delta)
+        if ((threadIdx.x & 31) == 0) cnt[u] = n | (dir == 0 && !(omax[u] <= GRAD_EXACT * least) ? GRAD_FLAG : 0);
     }
     for (int i = threadIdx.x; i <= nb; i += blockDim.x) go_start[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < ngroups; i += blockDim.x) atomicAdd(&go_start[nb - cnt[i]], 1);
+    for (int i = threadIdx.x; i < ngroups; i += blockDim.x) atomicAdd(&go_start[nb - (cnt[i] & ~GRAD_FLAG)], 1);
     __syncthreads();
     if (threadIdx.x < 32) {   // exclusive scan over descending lengths
         int base = 0;
@@ -1014,14 +1033,8 @@ __global__ void __launch_bounds__(LISTS_THREADS) grad_lists_kernel(Geo g, int G,
     }
     __syncthreads();
     for (int i = threadIdx.x; i < ngroups; i += blockDim.x) {
-        int entry = i | (cnt[i] << 12);
-        if (dir == 0) {
-            const int at = i * G * g.bs / 8, n = min(G * g.bs / 8, n8 - at);
-            float o2 = 0.f;
-            for (int k = 0; k < n; ++k) o2 = fmaxf(o2, norms[at + k].x);
-            if (!(o2 <= limit)) entry |= GRAD_FLAG;   // (a mean that is not finite: every tile)
-        }
-        ord[atomicAdd(&go_start[nb - cnt[i]], 1)] = entry;
+        const int n = cnt[i] & ~GRAD_FLAG;
+        ord[atomicAdd(&go_start[nb - n], 1)] = i | (n << 12) | (cnt[i] & GRAD_FLAG);
     }
 }
 
@@ -1111,7 +1124,7 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
                           ndelta, norms, bits, ext);
     if (rc != FVATTN_OK) return rc;
     rc = launch_after(grad_lists_kernel, static_cast<unsigned>(2 * BH), LISTS_THREADS,
-                          sizeof(int) * (g.nb + 1 + wl.ngroups), s, g, wl.G, wl.ngroups, wl.nwords, bits, norms, ulq,
+                          sizeof(int) * (2 * g.nb + 1 + 2 * wl.ngroups), s, g, wl.G, wl.ngroups, wl.nwords, bits, norms, ulq,
                           ulk, ordq, ordk, counters);
     if (rc != FVATTN_OK) return rc;
 

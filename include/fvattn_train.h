@@ -45,10 +45,10 @@ size_t fvattn_sparse_attn_bwd_workspace_size(const fvattn_geom *g);
  * sum in dS is dO_t . O_t in exact arithmetic; it is formed from P where the
  * bf16 O is too coarse for it.  No atomics touch a result: the output bits
  * depend only on the inputs, not on the schedule nor on how heads are split
- * across calls.  Blocks that no list holds are not read.  A NaN or infinity in
- * a block reaches the rows and keys paired with it and, with blocks below 128
- * tokens, those of the other blocks in the same 128 rows (as in
- * fvattn_sparse_attn).
+ * across calls.  K and V of blocks that no list holds change no bit of them,
+ * whatever they hold.  A NaN or infinity in a block reaches the rows and keys
+ * paired with it and, with blocks below 128 tokens, those of the other blocks
+ * in the same 128 rows (as in fvattn_sparse_attn).
  *   q_t, k_t, v_t, do_t  [B, H, Npad, D] bf16 from fvattn_reorder (padding
  *                        rows zero)
  *   o_t, lse             as fvattn_sparse_attn_lse wrote them for the same

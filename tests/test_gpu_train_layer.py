@@ -460,3 +460,59 @@ def test_nan_stays_in_its_head(fv, tr, geo):  # noqa: F811
         for a, b in zip(run(), want):
             assert torch.equal(a[:, 3:], b[:, 3:])
     assert fv.get_status() == 0
+
+
+def test_values_that_no_list_holds_change_no_bit(fv, tr):  # noqa: F811
+    """Concentrated rows, and values 25 times as large, or keys and values that are NaN, in the blocks that no list
+    holds: the same bits."""
+    for geo in ((1, 2, 64, 4, 16, 24, 2, 8, 8), (1, 2, 64, 4, 16, 24, 1, 4, 4)):
+        g = fv.geom(*geo)
+        last = g.nb - 128 // g.bs                   # whole tiles of blocks
+        idx, cnt = random_lists(g, 0.9, 2)
+        cnt = cnt.clamp(max=last)
+        idx[..., :last] = torch.arange(last, dtype=torch.int32, device="cuda")
+        q, k, v, do = tiles(g, 3, (3.0, 1.0, 1.0, 1.0))
+        o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+        want = tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt)
+        for factor in (25.0, float("nan")):
+            v[:, :, last * g.bs:] *= factor
+            k[:, :, last * g.bs:] *= factor / 25
+            for a, b in zip(tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt), want):
+                assert torch.equal(bits(a), bits(b))
+        assert fv.get_status() == 0
+
+
+@pytest.mark.parametrize("large", ["none", "no list holds them", "hardly weighted"])
+def test_concentrated_rows_beside_large_values(fv, tr, large):  # noqa: F811
+    """Scores of standard deviation 3 and some values 25 or 100 times the others', in blocks that no list holds, or
+    on four keys that are zero, which rows give next to no weight.  dQ's error a row, relative to the row: the
+    result's rounding r0 (measured on the 64-bit result), and independently dS's, r0 sqrt(sum_u |dS_tu k_u|^2),
+    with up to a ninth more of it (in squares) in rows that take delta from the rounded O.  So the rows' root mean
+    square is at most r0 sqrt(1 + (1 + 1/9) c), c the mean of sum_u |dS_tu k_u|^2 / |dQ_t|^2; 5% for chance.  Rows
+    with a probability above 0.9 are left out: there dP - delta cancels further than fp32 goes."""
+    g = fv.geom(1, 2, 64, 4, 16, 24, 2, 8, 8)
+    idx, cnt = random_lists(g, 1.0, 2)
+    last = g.nb - 1
+    cnt.fill_(last)
+    idx[..., :last] = torch.arange(last, dtype=torch.int32, device="cuda")
+    q, k, v, do = tiles(g, 3, (3.0, 1.0, 1.0, 1.0))
+    if large == "no list holds them":
+        v[:, :, last * g.bs:] *= 25
+    elif large == "hardly weighted":
+        v[:, :, 700:704] *= 100
+        k[:, :, 700:704] = 0
+    scale = 1 / math.sqrt(g.D)
+    o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+    got = tr.sparse_attn_bwd(g, q, k, v, o, do, lse, idx, cnt)[0].double()
+    n = last * g.bs
+    q, k, v, do = q.double(), k[:, :, :n].double(), v[:, :, :n].double(), do.double()
+    p = torch.softmax(q @ k.transpose(-1, -2) * scale, -1)
+    dp = do @ v.transpose(-1, -2)
+    ds = scale * p * (dp - (p * dp).sum(-1, keepdim=True))
+    dq = ds @ k
+    rows = p.amax(-1) < 0.9
+    assert rows.double().mean() > 0.9
+    rms = lambda e: ((e.square().sum(-1) / dq.square().sum(-1))[rows].mean().sqrt()).item()  # noqa: E731
+    c = ((ds.square() @ k.square().sum(-1, keepdim=True)).squeeze(-1) / dq.square().sum(-1))[rows].mean().item()
+    assert rms(got - dq) <= 1.05 * math.sqrt(1 + (1 + 1 / 9) * c) * rms(dq.to(BF16).double() - dq)
+    assert fv.get_status() == 0
