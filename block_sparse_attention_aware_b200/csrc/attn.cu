@@ -517,15 +517,16 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl.mrg_empty));
             const float mm = fmaxf(m0, m1);
-            // a group with no chunk in this item has l = 0 and m = -inf: weight 0
-            const float a0 = l0 > 0.f ? ex2_approx(m0 - mm) : 0.f;
-            const float a1 = l1 > 0.f ? ex2_approx(m1 - mm) : 0.f;
+            // a group with no chunk in this item has l = 0 and m = -inf: weight 0.  (A NaN score makes l NaN,
+            // and O with it.)
+            const float a0 = l0 != 0.f ? ex2_approx(m0 - mm) : 0.f;
+            const float a1 = l1 != 0.f ? ex2_approx(m1 - mm) : 0.f;
             // Which group holds which half of an item's chunks follows the CTA's chunk count, so the
             // merge is written symmetric in the two groups (products rounded separately, one add;
             // no contraction into an fma): the output bits do not depend on the schedule.
             const float inv = 1.0f / __fadd_rn(__fmul_rn(l0, a0), __fmul_rn(l1, a1));
             const float f0 = a0 * inv, f1 = a1 * inv;
-            const bool use0 = __any_sync(0xffffffffu, l0 > 0.f), use1 = __any_sync(0xffffffffu, l1 > 0.f);
+            const bool use0 = __any_sync(0xffffffffu, l0 != 0.f), use1 = __any_sync(0xffffffffu, l1 != 0.f);
             tc_fence_after();
             const bool in_tile = GRP ? row < min(a.G, g.nb - qb) * bs : row < bs;   // rows of real query blocks
             __nv_bfloat16* orow;
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                     uint32_t o0[32];
                     tmem_ld32(trow + O_COL + col, o0);
                     tmem_wait_ld();
-                    if (l0 > 0.f) {
+                    if (l0 != 0.f) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) r[i] = __fmul_rn(__uint_as_float(o0[i]), f0);
                     }
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                     uint32_t o1[32];
                     tmem_ld32(trow + O_COL + 128u + col, o1);
                     tmem_wait_ld();
-                    if (l1 > 0.f) {
+                    if (l1 != 0.f) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) r1[i] = __fmul_rn(__uint_as_float(o1[i]), f1);
                     }

@@ -516,3 +516,31 @@ def test_concentrated_rows_beside_large_values(fv, tr, large):  # noqa: F811
     c = ((ds.square() @ k.square().sum(-1, keepdim=True)).squeeze(-1) / dq.square().sum(-1))[rows].mean().item()
     assert rms(got - dq) <= 1.05 * math.sqrt(1 + (1 + 1 / 9) * c) * rms(dq.to(BF16).double() - dq)
     assert fv.get_status() == 0
+
+
+@pytest.mark.parametrize("keep", [1, 3], ids=["one chunk", "three chunks"])
+def test_nan_scores_are_not_taken_for_an_empty_row(fv, tr, keep):  # noqa: F811
+    """A row whose query holds a NaN, and rows that keep a block of keys with one: O and lse are NaN as the formula's
+    are (O = 0 and lse = -inf are for rows that keep nothing); the other rows have the bits that they have without."""
+    g = fv.geom(1, 1, 128, 2, 16, 64, 2, 8, 8)
+    idx, cnt = random_lists(g, 1.0, 1)
+    cnt.fill_(keep)
+    cnt[0, 0, 5] = 0
+    for i in range(g.nb):
+        idx[0, 0, i, :keep] = torch.arange(keep, dtype=torch.int32) + (1 if i < 8 else 10)
+    q, k, v, _ = tiles(g, 2)
+    o, lse = tr.sparse_attn_lse(g, q, k, v, idx, cnt)
+    rows = torch.arange(g.Npad, device="cuda")
+    bad = (rows == 3) | ((rows >= 130) & (rows < 258)) | (rows == 5 * g.bs)
+    q[0, 0, bad, 7] = float("nan")
+    k[0, 0, 10 * g.bs + 9, 0] = float("nan")       # the blocks 8 .. keep it
+    nan = ((bad & (rows // g.bs < 8)) | (rows >= 8 * g.bs)) & (rows // g.bs != 5)
+    for got, l in ((tr.sparse_attn_lse(g, q, k, v, idx, cnt)), (fv.sparse_attn(g, q, k, v, idx, cnt.clamp(min=1)), None)):
+        got, want = got[0, 0], o[0, 0]
+        assert got[nan].isnan().all()
+        fine = ~nan & (rows // g.bs != 5)
+        assert torch.equal(bits(got[fine]), bits(want[fine]))
+        if l is not None:
+            assert l[0, 0, nan].isnan().all() and torch.equal(l[0, 0, ~nan], lse[0, 0, ~nan])
+            assert (got[rows // g.bs == 5] == 0).all()
+    assert fv.get_status() == 0
