@@ -26,7 +26,7 @@ from . import fvattn, train
 from .fvattn import _check
 from .train import _check_call, _need, _need_workspace, _on
 
-EXPORTED = ("fvattn_cache_append", "fvattn_cache_attn_parts", "fvattn_cache_attn_workspace_size",
+EXPORTED = ("fvattn_cache_append", "fvattn_cache_append_fresh", "fvattn_cache_attn_parts", "fvattn_cache_attn_workspace_size",
             "fvattn_cache_attn")
 
 BF16, I32, F32 = torch.bfloat16, torch.int32, torch.float32
@@ -54,8 +54,9 @@ def load():
         L = fvattn.load()
         P, I, LL, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
         C, R = ctypes.POINTER(_Cache), ctypes.POINTER(_Rotation)
-        L.fvattn_cache_append.argtypes = [C, I, LL, P, P, P, I, P, LL, P, LL, P, LL, I, P, LL, R, P]
-        L.fvattn_cache_append.restype = I
+        for call in (L.fvattn_cache_append, L.fvattn_cache_append_fresh):
+            call.argtypes = [C, I, LL, P, P, P, I, P, LL, P, LL, P, LL, I, P, LL, R, P]
+            call.restype = I
         L.fvattn_cache_attn_parts.argtypes = [I, I, I, I, LL, ctypes.POINTER(I)]
         L.fvattn_cache_attn_parts.restype = I
         L.fvattn_cache_attn_workspace_size.argtypes = [I, I, I, I, LL]
@@ -138,7 +139,9 @@ class PagedCache:
         sequences.  Sequence b's are rows cu[b] .. cu[b+1]-1 (cu None: row b),
         and lens[b] counts them.  With `rot` (rotation_table) and `pos`
         ([rows, len(axes)] int32) the keys, and the queries q ([rows, Hq, D])
-        into q_out, are rotated; q_out may be q.  Returns q_out."""
+        into q_out, are rotated; q_out may be q.  Returns q_out.  Rows of no
+        sequence and refused tokens are left alone in a q_out that is given,
+        and zero in one made here."""
         if stream is None:
             done = (train._fast or train.native()).append(
                 self.k_pages, self.v_pages, k, v, table, lens, cu, q, q_out, pos, rot,
@@ -178,16 +181,17 @@ class PagedCache:
             raise ValueError("pos and axes belong with rot")
         L = load()
         with _on(self.device, stream) as s:
+            call = L.fvattn_cache_append
             if q is not None and q_out is None:
+                call = L.fvattn_cache_append_fresh
                 q_out = torch.empty((rows, hq, self.D), dtype=BF16, device=self.device)
                 qos = hq * self.D
             if rows == 0:
                 return q_out
-            rc = L.fvattn_cache_append(ctypes.byref(self._c), B, rows, None if cu is None else cu.data_ptr(),
-                                       lens.data_ptr(), table.data_ptr(), width, k.data_ptr(), ks, v.data_ptr(), vs,
-                                       None if q is None else q.data_ptr(), qs, hq,
-                                       None if q is None else q_out.data_ptr(), qos,
-                                       None if r is None else ctypes.byref(r), s)
+            rc = call(ctypes.byref(self._c), B, rows, None if cu is None else cu.data_ptr(),
+                      lens.data_ptr(), table.data_ptr(), width, k.data_ptr(), ks, v.data_ptr(), vs,
+                      None if q is None else q.data_ptr(), qs, hq, None if q is None else q_out.data_ptr(), qos,
+                      None if r is None else ctypes.byref(r), s)
             if rc:
                 _check("fvattn_cache_append", rc)
         return q_out

@@ -168,9 +168,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         qo = &made;
         qos = hq * c.D;
     }
-    if (fvattn_cache_append(&c, static_cast<int>(B), rows, ptr<int32_t>(cu), ptr<int32_t>(lens), ptr<int32_t>(table),
-                            static_cast<int>(table->size(1)), k->data_ptr(), ks, v->data_ptr(), vs, ptr<void>(q), qs,
-                            static_cast<int>(hq), ptr<void>(qo), qos, rot ? &r : nullptr, stream_of(dev)) != FVATTN_OK)
+    const auto call = made.defined() ? fvattn_cache_append_fresh : fvattn_cache_append;
+    if (call(&c, static_cast<int>(B), rows, ptr<int32_t>(cu), ptr<int32_t>(lens), ptr<int32_t>(table),
+             static_cast<int>(table->size(1)), k->data_ptr(), ks, v->data_ptr(), vs, ptr<void>(q), qs,
+             static_cast<int>(hq), ptr<void>(qo), qos, rot ? &r : nullptr, stream_of(dev)) != FVATTN_OK)
         return not_here();
     if (made.defined()) return THPVariable_Wrap(std::move(made));
     PyObject* out = q ? a[8] : Py_None;

@@ -42,7 +42,7 @@ namespace fv {
 struct AppendArgs {
     int Hq, Hkv, page, pages, B, width, axes;
     int pair_end[3];              // first pair past each axis
-    int rot_rows, halves;
+    int rot_rows, halves, fill;
     long long k_stride, v_stride, q_stride, q_out_stride;
     const int32_t *cu, *lens, *table, *pos;
     const float* rot;
@@ -107,7 +107,12 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
             bad = true;
         }
     }
-    if (__syncthreads_or(bad) || !s_ok) return;
+    if (__syncthreads_or(bad) || !s_ok) {
+        if (a.fill)                      // nobody else has written this row of q_out
+            for (int i = blockIdx.y * 256 + tid; i < a.Hq * D / 8; i += gridDim.y * 256)
+                reinterpret_cast<uint4*>(a.q_out + t * a.q_out_stride)[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
     const int u = tid % UPH;
     const int step = a.halves ? D / 2 : 8;       // distance of the unit's two vectors
     const int e0 = a.halves ? 8 * u : 16 * u;
@@ -691,11 +696,10 @@ static int launch_cache_attn(const CUtensorMap& tk, const CUtensorMap& tv, const
 
 using namespace fv;
 
-extern "C" int fvattn_cache_append(const fvattn_cache* c, int B, long long rows, const int32_t* cu,
-                                   const int32_t* lens, const int32_t* table, int width, const void* k,
-                                   long long k_stride, const void* v, long long v_stride, const void* q,
-                                   long long q_stride, int Hq, void* q_out, long long q_out_stride,
-                                   const fvattn_rotation* rot, fvattn_stream_t stream) {
+static int append_impl(const fvattn_cache* c, int B, long long rows, const int32_t* cu, const int32_t* lens,
+                       const int32_t* table, int width, const void* k, long long k_stride, const void* v,
+                       long long v_stride, const void* q, long long q_stride, int Hq, void* q_out,
+                       long long q_out_stride, const fvattn_rotation* rot, int fill, fvattn_stream_t stream) {
     if (!cache_ok(c) || B < 1 || rows < 0 || rows > 0x7fffffffll || width < 1 || !lens || !table || !k || !v)
         return FVATTN_ERR_INVALID;
     if (!cache_supported(c->D, c->page)) return FVATTN_ERR_UNSUPPORTED;
@@ -729,6 +733,7 @@ extern "C" int fvattn_cache_append(const fvattn_cache* c, int B, long long rows,
         a.pos = rot->pos;
     }
     if (rows == 0) return FVATTN_OK;
+    a.fill = fill;
     a.Hq = q ? Hq : 0;
     a.Hkv = c->Hkv;
     a.page = c->page;
@@ -755,6 +760,25 @@ extern "C" int fvattn_cache_append(const fvattn_cache* c, int B, long long rows,
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return c->D == 128 ? launch_after(cache_append_kernel<128>, grid, 256, 0, s, a)
                        : launch_after(cache_append_kernel<64>, grid, 256, 0, s, a);
+}
+
+extern "C" int fvattn_cache_append(const fvattn_cache* c, int B, long long rows, const int32_t* cu,
+                                   const int32_t* lens, const int32_t* table, int width, const void* k,
+                                   long long k_stride, const void* v, long long v_stride, const void* q,
+                                   long long q_stride, int Hq, void* q_out, long long q_out_stride,
+                                   const fvattn_rotation* rot, fvattn_stream_t stream) {
+    return append_impl(c, B, rows, cu, lens, table, width, k, k_stride, v, v_stride, q, q_stride, Hq, q_out, q_out_stride,
+                       rot, 0, stream);
+}
+
+extern "C" int fvattn_cache_append_fresh(const fvattn_cache* c, int B, long long rows, const int32_t* cu,
+                                         const int32_t* lens, const int32_t* table, int width, const void* k,
+                                         long long k_stride, const void* v, long long v_stride, const void* q,
+                                         long long q_stride, int Hq, void* q_out, long long q_out_stride,
+                                         const fvattn_rotation* rot, fvattn_stream_t stream) {
+    if (!q || q == q_out) return FVATTN_ERR_INVALID;
+    return append_impl(c, B, rows, cu, lens, table, width, k, k_stride, v, v_stride, q, q_stride, Hq, q_out, q_out_stride,
+                       rot, 1, stream);
 }
 
 extern "C" int fvattn_cache_attn_parts(int B, int Hq, int Hkv, int D, long long longest, int* tokens) {

@@ -61,7 +61,8 @@ typedef struct {
  *   table, width    [B, width] int32 page numbers; entries past a sequence's
  *                   last page are not read
  * A position outside the table, a token outside [0, width * page) and a page
- * outside the pool set FVATTN_ERR_BOUNDS, and that token is not written.
+ * outside the pool set FVATTN_ERR_BOUNDS, and that token is not written,
+ * neither to the pages nor to q_out.
  * Only the new tokens' rows of the pages change.  No two sequences may append
  * to one page.  Pointers 16-byte aligned (cu, lens, table and pos: 4). */
 int fvattn_cache_append(const fvattn_cache *c, int B, long long rows, const int32_t *cu, const int32_t *lens,
@@ -69,6 +70,15 @@ int fvattn_cache_append(const fvattn_cache *c, int B, long long rows, const int3
                         const void *k, long long k_stride, const void *v, long long v_stride,
                         const void *q, long long q_stride, int Hq, void *q_out, long long q_out_stride,
                         const fvattn_rotation *rot, fvattn_stream_t stream);
+
+/* fvattn_cache_append into a q_out that holds nothing yet: its rows that
+ * fvattn_cache_append leaves alone (rows of no sequence, refused tokens) get
+ * zero.  q is required, and q_out is not q. */
+int fvattn_cache_append_fresh(const fvattn_cache *c, int B, long long rows, const int32_t *cu, const int32_t *lens,
+                              const int32_t *table, int width,
+                              const void *k, long long k_stride, const void *v, long long v_stride,
+                              const void *q, long long q_stride, int Hq, void *q_out, long long q_out_stride,
+                              const fvattn_rotation *rot, fvattn_stream_t stream);
 
 /* Parts that fvattn_cache_attn splits a sequence's tokens into, for up to
  * `longest` tokens a sequence, and the tokens a part holds (a multiple of

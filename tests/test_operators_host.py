@@ -235,3 +235,15 @@ def test_kernels_that_start_early_read_with_plain_loads(name):
         src = "\n".join(parts)
     for path in (r"__ldg\s*\(", r"ld\.global\.nc", r"const\s+[\w:]+\s*\*\s*__restrict__"):
         assert not re.search(path, src), path
+
+
+def test_append_into_fresh_queries_refuses(mods):
+    fv, _, ca = mods
+
+    class Fresh:         # _append's call under the other name
+        def load(self):
+            L = ca.load()
+            return type("L", (), dict(fvattn_cache_append=staticmethod(L.fvattn_cache_append_fresh)))
+
+    for kw in (dict(q=None, qo=None), dict(q=None), dict(qo=None), dict(q=A, qo=A), dict(B=0, qo=2 * A), dict(qos=100, qo=2 * A)):
+        assert _append(Fresh(), ca, **kw) == fv.ERR_INVALID, kw
