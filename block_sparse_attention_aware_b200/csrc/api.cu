@@ -101,7 +101,7 @@ extern "C" int fvattn_block_order(const fvattn_geom* g, int32_t* table, fvattn_s
 
 extern "C" int fvattn_get_status(fvattn_stream_t stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaStreamSynchronize(s) != cudaSuccess) return FVATTN_ERR_CUDA;
+    if (!cuda_ok(cudaStreamSynchronize(s))) return FVATTN_ERR_CUDA;
     // every word is read and cleared; the attention kernels' error is reported first
     const int va = take_status_attn();
     const int vr = take_status_route();
@@ -138,5 +138,5 @@ extern "C" int fvattn_copy_heads(const fvattn_geom* g, int h0, int nh, const voi
     else
         e = cudaMemcpy2DAsync(static_cast<char*>(dst) + row * h0, full, src, part, part, rows,
                               cudaMemcpyDeviceToHost, s);
-    return e == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA;
+    return cuda_ok(e) ? FVATTN_OK : FVATTN_ERR_CUDA;
 }

@@ -1089,8 +1089,8 @@ static std::atomic<int> g_hook_flags{0};
 
 static int cached_num_sms() {
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (!cuda_ok(cudaGetDevice(&dev))) return 0;
+    if (!cuda_ok(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev))) return 0;
     return n;
 }
 
@@ -1102,16 +1102,16 @@ static int launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
     using L = Smem<D>;
     static std::atomic<unsigned long long> ready{0};   // devices on which the kernel has its shared memory
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return FVATTN_ERR_CUDA;
+    if (!cuda_ok(cudaGetDevice(&dev))) return FVATTN_ERR_CUDA;
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
     if ((ready.load(std::memory_order_relaxed) & bit) == 0ull) {
-        if (cudaFuncSetAttribute(sparse_attn_kernel<D, GRP, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(L::ALLOC)) != cudaSuccess)
+        if (!cuda_ok(cudaFuncSetAttribute(sparse_attn_kernel<D, GRP, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          static_cast<int>(L::ALLOC))))
             return FVATTN_ERR_CUDA;
         // The warpgroups' register shares (setmaxnreg) must fit in what a CTA is
         // launched with, or the raising warpgroups would wait for ever.
         cudaFuncAttributes fa;
-        if (cudaFuncGetAttributes(&fa, sparse_attn_kernel<D, GRP, LSE>) != cudaSuccess) return FVATTN_ERR_CUDA;
+        if (!cuda_ok(cudaFuncGetAttributes(&fa, sparse_attn_kernel<D, GRP, LSE>))) return FVATTN_ERR_CUDA;
         if (static_cast<long long>(fa.numRegs) * ATT_THREADS < 128ll * RegSplit<GRP>::LOW + 256ll * RegSplit<GRP>::HIGH)
             return FVATTN_ERR_UNSUPPORTED;
         ready.fetch_or(bit, std::memory_order_relaxed);

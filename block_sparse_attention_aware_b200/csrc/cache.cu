@@ -662,10 +662,10 @@ static size_t attn_ws(int B, int Hq, int D, int parts) {
 static int current_sms(int* device = nullptr) {
     static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (!cuda_ok(cudaGetDevice(&dev))) return 148;
     if (device) *device = dev;
     if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+    if (!cuda_ok(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) || n <= 0) return 148;
     if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
@@ -677,8 +677,8 @@ static int launch_cache_attn(const CUtensorMap& tk, const CUtensorMap& tv, const
     static std::atomic<unsigned long long> ready{0};   // devices on which the kernel has its shared memory
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
     if ((ready.load(std::memory_order_relaxed) & bit) == 0ull) {
-        if (cudaFuncSetAttribute(cache_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(L::TOTAL)) != cudaSuccess)
+        if (!cuda_ok(cudaFuncSetAttribute(cache_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          static_cast<int>(L::TOTAL))))
             return FVATTN_ERR_CUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }

@@ -39,13 +39,22 @@ __device__ __forceinline__ void record_status(int code) {
     atomicCAS(&g_tu_status, 0, code);
 }
 
+// Host side: whether a runtime call went well.  The error of one that did not
+// is in what the entry point returns, and cleared as the runtime's last one,
+// which the next check of another's launch would take for its own.
+static inline bool cuda_ok(cudaError_t e) {
+    if (e == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+}
+
 // Host side: read this translation unit's status word on the current device
 // and clear it; FVATTN_ERR_CUDA if the copy fails.
 static inline int take_tu_status() {
     int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_tu_status, sizeof(int)) != cudaSuccess) return FVATTN_ERR_CUDA;
+    if (!cuda_ok(cudaMemcpyFromSymbol(&v, g_tu_status, sizeof(int)))) return FVATTN_ERR_CUDA;
     const int zero = 0;
-    if (cudaMemcpyToSymbol(g_tu_status, &zero, sizeof(int)) != cudaSuccess) return FVATTN_ERR_CUDA;
+    if (!cuda_ok(cudaMemcpyToSymbol(g_tu_status, &zero, sizeof(int)))) return FVATTN_ERR_CUDA;
     return v;
 }
 
@@ -69,7 +78,7 @@ static int launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t 
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? FVATTN_OK : FVATTN_ERR_CUDA;
+    return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...)) ? FVATTN_OK : FVATTN_ERR_CUDA;
 }
 
 // The status words of the files whose kernels record errors.

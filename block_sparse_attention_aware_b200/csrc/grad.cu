@@ -1074,12 +1074,12 @@ static int launch_grad(const CUtensorMap& a0, const CUtensorMap& a1, const CUten
     static std::atomic<unsigned long long> ready{0};   // devices on which the kernel has its shared memory
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
     if ((ready.load(std::memory_order_relaxed) & bit) == 0ull) {
-        if (cudaFuncSetAttribute(grad_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(L::ALLOC)) != cudaSuccess)
+        if (!cuda_ok(cudaFuncSetAttribute(grad_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          static_cast<int>(L::ALLOC))))
             return FVATTN_ERR_CUDA;
         // setmaxnreg waits for ever for registers that the CTA was not launched with
         cudaFuncAttributes fa;
-        if (cudaFuncGetAttributes(&fa, grad_kernel<D, KV>) != cudaSuccess) return FVATTN_ERR_CUDA;
+        if (!cuda_ok(cudaFuncGetAttributes(&fa, grad_kernel<D, KV>))) return FVATTN_ERR_CUDA;
         if (static_cast<long long>(fa.numRegs) * GRAD_THREADS < 128ll * (GRAD_LOW + GRAD_GROUPS * GRAD_HIGH))
             return FVATTN_ERR_UNSUPPORTED;
         ready.fetch_or(bit, std::memory_order_relaxed);
@@ -1112,8 +1112,8 @@ static int grad_launches(const Geo& g, const GradWs& wl, const void* q_t, const 
     };
     if (!tmap(&tq, q_t) || !tmap(&tk, k_t) || !tmap(&tv, v_t) || !tmap(&tdo, do_t)) return FVATTN_ERR_CUDA;
     int dev = 0, nsm = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    if (!cuda_ok(cudaGetDevice(&dev)) ||
+        !cuda_ok(cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)))
         return FVATTN_ERR_CUDA;
 
     const int stat_blocks = static_cast<int>((rows + 63) / 64);

@@ -27,14 +27,14 @@ static std::mutex g_scratch_mutex;
 
 static int scratch_on_current_device(void** out) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return FVATTN_ERR_CUDA;
+    if (!cuda_ok(cudaGetDevice(&dev))) return FVATTN_ERR_CUDA;
     if (dev < 0 || dev >= kMaxDevices) return FVATTN_ERR_UNSUPPORTED;
     std::lock_guard<std::mutex> lock(g_scratch_mutex);
     if (!g_scratch_ptr[dev]) {
         void* p = nullptr;
         // In host code g_noalloc_scratch names a host-side stand-in; the
         // device address must come from the runtime.
-        if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || !p) return FVATTN_ERR_CUDA;
+        if (!cuda_ok(cudaGetSymbolAddress(&p, g_noalloc_scratch)) || !p) return FVATTN_ERR_CUDA;
         g_scratch_ptr[dev] = p;
     }
     *out = g_scratch_ptr[dev];

@@ -711,8 +711,7 @@ static int launch_select(long long rows, int nb, const float* L, double p, int k
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, select_kernel<NPL, KEEP_E>, nb, rows, L, p, kfloor, kextra, kv_idx, kv_cnt) !=
-        cudaSuccess)
+    if (!cuda_ok(cudaLaunchKernelEx(&cfg, select_kernel<NPL, KEEP_E>, nb, rows, L, p, kfloor, kextra, kv_idx, kv_cnt)))
         return FVATTN_ERR_CUDA;
     FV_CHECK_LAUNCH();
     return FVATTN_OK;
@@ -743,8 +742,8 @@ static RouteWs route_ws(const fvattn_geom& g) {
 
 static int score_sms() {
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (!cuda_ok(cudaGetDevice(&dev))) return 0;
+    if (!cuda_ok(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev))) return 0;
     return n;
 }
 
@@ -835,8 +834,7 @@ static int route_impl(const fvattn_geom* gp, const void* q_raster, const void* k
     sa.tiles = static_cast<long long>(g.B) * g.H * sa.m_tiles * sa.n_tiles;
     const int nsm = score_sms();
     if (nsm <= 0) return FVATTN_ERR_CUDA;
-    if (cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SC_SMEM)) !=
-        cudaSuccess)
+    if (!cuda_ok(cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SC_SMEM))))
         return FVATTN_ERR_CUDA;
     const unsigned sgrid = static_cast<unsigned>(sa.tiles < nsm ? sa.tiles : nsm);
     {
@@ -851,7 +849,7 @@ static int route_impl(const fvattn_geom* gp, const void* q_raster, const void* k
         cfg.stream = s;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, score_kernel, tqh, tql, tkh, tkl, tout, sa) != cudaSuccess) return FVATTN_ERR_CUDA;
+        if (!cuda_ok(cudaLaunchKernelEx(&cfg, score_kernel, tqh, tql, tkh, tkl, tout, sa))) return FVATTN_ERR_CUDA;
     }
     FV_CHECK_LAUNCH();
     const long long rows = static_cast<long long>(g.B) * g.H * g.nb;

@@ -247,3 +247,100 @@ def test_append_into_fresh_queries_refuses(mods):
 
     for kw in (dict(q=None, qo=None), dict(q=None), dict(qo=None), dict(q=A, qo=A), dict(B=0, qo=2 * A), dict(qos=100, qo=2 * A)):
         assert _append(Fresh(), ca, **kw) == fv.ERR_INVALID, kw
+
+
+# ------------------------------------------------------------------ errors
+
+# A stand-in for the CUDA runtime whose calls fail as often as it is told: it runs nothing and keeps the last error as
+# the runtime does.
+FAKE_RUNTIME = r"""
+#include <stddef.h>
+static int last = 0, left = 0;
+void fake_fail_after(int calls) { left = calls; last = 0; }
+int fake_last(void) { return last; }
+static int result(void) { if (left-- > 0) return 0; return last = 719; }
+int cudaGetLastError(void) { int e = last; last = 0; return e; }
+int cudaGetDevice(int* d) { *d = 0; return result(); }
+int cudaDeviceGetAttribute(int* v, int attr, int dev) { (void)attr; (void)dev; *v = 148; return result(); }
+int cudaFuncGetAttributes(int* a, const void* f) { (void)f; for (int i = 0; i < 16; ++i) a[i] = 255; return result(); }
+int cudaFuncSetAttribute(const void* f, int a, int v) { (void)f; (void)a; (void)v; return result(); }
+static int encode(void) { return 0; }
+int cudaGetDriverEntryPoint(const char* n, void** p, unsigned long long f, int* q) { (void)n; (void)f; *p = (void*)encode; *q = 0; return result(); }
+int cudaGetSymbolAddress(void** p, const void* s) { (void)s; *p = (void*)4096; return result(); }
+int cudaLaunchKernel(void) { return result(); }
+int cudaLaunchKernelExC(void) { return result(); }
+int cudaMemcpy2DAsync(void) { return result(); }
+int cudaMemcpyFromSymbol(int* d) { *d = 0; return result(); }
+int cudaMemcpyToSymbol(void) { return result(); }
+int cudaStreamSynchronize(void) { return result(); }
+int __cudaPushCallConfiguration(void) { return 0; }
+int __cudaPopCallConfiguration(void) { return 0; }
+static void* handle[4];
+void** __cudaRegisterFatBinary(void* f) { (void)f; return handle; }
+void __cudaRegisterFatBinaryEnd(void** h) { (void)h; }
+void __cudaUnregisterFatBinary(void** h) { (void)h; }
+void __cudaRegisterFunction(void) {}
+void __cudaRegisterVar(void) {}
+"""
+
+CALLER = r"""
+import ctypes, sys
+fake, path = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL), sys.argv[2]
+L = ctypes.CDLL(path)
+I, P, F, LL, D, S = ctypes.c_int, ctypes.c_void_p, ctypes.c_float, ctypes.c_longlong, ctypes.c_double, ctypes.c_size_t
+A, BIG = P(4096), S(1 << 40)
+geoms = []
+for bs in ((2, 2, 4), (2, 8, 8)):
+    g = ctypes.create_string_buffer(256)
+    ctypes.memmove(g, (I * 9)(1, 2, 64, 4, 16, 16, *bs), 36)
+    assert L.fvattn_geom_init(g) == 0
+    geoms.append(g)
+cache = ctypes.create_string_buffer(64)
+ctypes.memmove(cache, (I * 4)(4, 2, 64, 16), 16)
+ctypes.memmove(ctypes.byref(cache, 16), (P * 2)(4096, 8192), 16)
+calls = {}
+for n, g in enumerate(geoms):
+    calls.update({
+        f"lse {n}": lambda g=g: L.fvattn_sparse_attn_lse(g, A, A, A, A, A, F(0.125), A, A, None, A, BIG, None),
+        f"attn {n}": lambda g=g: L.fvattn_sparse_attn(g, A, A, A, A, A, F(0.125), A, None, A, BIG, None),
+        f"noalloc {n}": lambda g=g: L.fvattn_sparse_attn_noalloc(g, A, A, A, A, A, F(0.125), A, None, None),
+        f"bwd {n}": lambda g=g: L.fvattn_sparse_attn_bwd(g, A, A, A, A, A, A, A, A, F(0.125), A, A, A, A, BIG, None),
+        f"route {n}": lambda g=g: L.fvattn_route(g, A, A, D(0.9), I(1), F(0.125), A, A, None, None, None, A, BIG, None),
+        f"reorder_route {n}": lambda g=g: L.fvattn_reorder_route(g, A, A, A, P(8192), D(0.9), I(1), I(0), F(0.125), A, A, None,
+                                                                None, None, A, BIG, None),
+        f"reorder {n}": lambda g=g: L.fvattn_reorder(g, A, P(8192), None),
+        f"order {n}": lambda g=g: L.fvattn_block_order(g, A, None),
+        f"heads {n}": lambda g=g: L.fvattn_copy_heads(g, I(0), I(1), A, P(8192), I(1), None)})
+calls["append"] = lambda: L.fvattn_cache_append(cache, I(2), LL(2), None, A, A, I(2), A, LL(128), A, LL(128), None, LL(0), I(0), None,
+                                                LL(0), None, None)
+calls["attend"] = lambda: L.fvattn_cache_attn(cache, I(2), I(4), A, LL(256), A, I(2), A, LL(5000), F(0.125), A, A, A, BIG, None)
+calls["status"] = lambda: L.fvattn_get_status(None)
+for name, call in calls.items():
+    for good in range(40):           # the runtime's calls fail from the good-th on
+        fake.fake_fail_after(good)
+        rc = call()
+        assert fake.fake_last() == 0, (name, good, rc)
+        if rc == 0:
+            break
+        assert rc == 3, (name, good, rc)
+    else:
+        raise AssertionError(name)
+    assert good > 0, name
+print("done")
+"""
+
+
+def test_failed_calls_leave_no_error_behind(mods, tmp_path):
+    """Whichever call of the runtime fails, the entry point returns the error and clears the runtime's last one, which
+    the next check of somebody else's launch would take for its own."""
+    import subprocess
+    import sys
+    from block_sparse_attention_aware_b200 import fvattn
+    src, lib = tmp_path / "fake.c", tmp_path / "libcudart.so.12"
+    src.write_text(FAKE_RUNTIME)
+    (tmp_path / "versions").write_text("libcudart.so.12 { global: *; };")
+    subprocess.check_call(["gcc", "-shared", "-fPIC", "-O1", "-w", "-Wl,-soname,libcudart.so.12",
+                           f"-Wl,--version-script={tmp_path}/versions", str(src), "-o", str(lib)])
+    done = subprocess.run([sys.executable, "-S", "-c", CALLER, str(lib), fvattn.LIB_PATH], capture_output=True, text=True, timeout=120,
+                          env=dict(os.environ, LD_LIBRARY_PATH=str(tmp_path)))
+    assert done.returncode == 0 and "done" in done.stdout, done.stderr[-2000:]
