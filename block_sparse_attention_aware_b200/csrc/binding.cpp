@@ -7,7 +7,9 @@
 // stream.  They serve the plain case only and answer NotImplemented to all
 // else: another device than the current one, wrong types or shapes, an error
 // of the C call.  The Python binding then goes its own way, which has the
-// messages.  No argument is kept.
+// messages.  No argument is kept.  Python's lock is given up while outputs are
+// made and kernels launched: both may wait, for memory or for room in the launch
+// queue, and what they wait for may be a function on the stream that needs it.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -26,6 +28,15 @@ namespace {
 using at::Tensor;
 
 PyObject* not_here() { Py_RETURN_NOTIMPLEMENTED; }
+
+// Python's lock, given up for a scope (which an exception may leave).
+struct Unlocked {
+    PyThreadState* const state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    Unlocked& operator=(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 // A tensor argument, or null for None; `ok` falls for anything else.
 const Tensor* arg(PyObject* o, bool& ok) {
@@ -163,16 +174,20 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return not_here();
     }
     Tensor made;
-    if (q && !qo) {
-        made = at::empty({rows, hq, c.D}, on(dev, at::kBFloat16));
-        qo = &made;
-        qos = hq * c.D;
+    int rc;
+    {
+        Unlocked unlocked;
+        if (q && !qo) {
+            made = at::empty({rows, hq, c.D}, on(dev, at::kBFloat16));
+            qo = &made;
+            qos = hq * c.D;
+        }
+        const auto call = made.defined() ? fvattn_cache_append_fresh : fvattn_cache_append;
+        rc = call(&c, static_cast<int>(B), rows, ptr<int32_t>(cu), ptr<int32_t>(lens), ptr<int32_t>(table),
+                  static_cast<int>(table->size(1)), k->data_ptr(), ks, v->data_ptr(), vs, ptr<void>(q), qs,
+                  static_cast<int>(hq), ptr<void>(qo), qos, rot ? &r : nullptr, stream_of(dev));
     }
-    const auto call = made.defined() ? fvattn_cache_append_fresh : fvattn_cache_append;
-    if (call(&c, static_cast<int>(B), rows, ptr<int32_t>(cu), ptr<int32_t>(lens), ptr<int32_t>(table),
-             static_cast<int>(table->size(1)), k->data_ptr(), ks, v->data_ptr(), vs, ptr<void>(q), qs,
-             static_cast<int>(hq), ptr<void>(qo), qos, rot ? &r : nullptr, stream_of(dev)) != FVATTN_OK)
-        return not_here();
+    if (rc != FVATTN_OK) return not_here();
     if (made.defined()) return THPVariable_Wrap(std::move(made));
     PyObject* out = q ? a[8] : Py_None;
     Py_INCREF(out);
@@ -224,18 +239,22 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         (ws && !dense(ws, dev, at::kByte, {ws->numel()})) || hq > 0x7fffffff || B > 65535)
         return not_here();
     Tensor made_out, made_lse, made_ws;
-    if (!ws) {
-        const size_t need = fvattn_cache_attn_workspace_size(static_cast<int>(B), static_cast<int>(hq), c.Hkv, c.D, longest);
-        if (need > 0) made_ws = at::empty({static_cast<long long>(need)}, on(dev, at::kByte));
+    int rc;
+    {
+        Unlocked unlocked;
+        if (!ws) {
+            const size_t need = fvattn_cache_attn_workspace_size(static_cast<int>(B), static_cast<int>(hq), c.Hkv, c.D, longest);
+            if (need > 0) made_ws = at::empty({static_cast<long long>(need)}, on(dev, at::kByte));
+        }
+        if (!out) made_out = at::empty({B, hq, c.D}, on(dev, at::kBFloat16));
+        if (!lse) made_lse = at::empty({B, hq}, on(dev, at::kFloat));
+        const Tensor* w = ws ? ws : (made_ws.defined() ? &made_ws : nullptr);
+        rc = fvattn_cache_attn(&c, static_cast<int>(B), static_cast<int>(hq), q->data_ptr(), qs, ptr<int32_t>(table),
+                               static_cast<int>(width), ptr<int32_t>(lens), longest, scale,
+                               out ? out->data_ptr() : made_out.data_ptr(), ptr<float>(lse ? lse : &made_lse),
+                               ptr<void>(w), w ? static_cast<size_t>(w->numel()) : 0, stream_of(dev));
     }
-    if (!out) made_out = at::empty({B, hq, c.D}, on(dev, at::kBFloat16));
-    if (!lse) made_lse = at::empty({B, hq}, on(dev, at::kFloat));
-    const Tensor* w = ws ? ws : (made_ws.defined() ? &made_ws : nullptr);
-    if (fvattn_cache_attn(&c, static_cast<int>(B), static_cast<int>(hq), q->data_ptr(), qs, ptr<int32_t>(table),
-                          static_cast<int>(width), ptr<int32_t>(lens), longest, scale,
-                          out ? out->data_ptr() : made_out.data_ptr(), ptr<float>(lse ? lse : &made_lse), ptr<void>(w),
-                          w ? static_cast<size_t>(w->numel()) : 0, stream_of(dev)) != FVATTN_OK)
-        return not_here();
+    if (rc != FVATTN_OK) return not_here();
     return pair(given(a[7], std::move(made_out)), given(a[8], std::move(made_lse)));
     END_HANDLE_TH_ERRORS
 }
@@ -265,14 +284,19 @@ PyObject* sparse_attn_lse(PyObject*, PyObject* const* a, Py_ssize_t n) {
         (lse && !dense(lse, dev, at::kFloat, {g.B, g.H, g.Npad})) || (ws && !dense(ws, dev, at::kByte, {ws->numel()})))
         return not_here();
     Tensor made_out, made_lse, made_ws;
-    if (!out) made_out = at::empty({g.B, g.H, g.Npad, g.D}, on(dev, at::kBFloat16));
-    if (!lse) made_lse = at::empty({g.B, g.H, g.Npad}, on(dev, at::kFloat));
-    if (!ws) made_ws = at::empty({static_cast<long long>(fvattn_attn_workspace_size(&g))}, on(dev, at::kByte));
-    const Tensor* w = ws ? ws : &made_ws;
-    if (fvattn_sparse_attn_lse(&g, q->data_ptr(), k->data_ptr(), v->data_ptr(), ptr<int32_t>(idx), ptr<int32_t>(cnt), scale,
-                               out ? out->data_ptr() : made_out.data_ptr(), ptr<float>(lse ? lse : &made_lse), nullptr,
-                               w->data_ptr(), static_cast<size_t>(w->numel()), stream_of(dev)) != FVATTN_OK)
-        return not_here();
+    int rc;
+    {
+        Unlocked unlocked;
+        if (!out) made_out = at::empty({g.B, g.H, g.Npad, g.D}, on(dev, at::kBFloat16));
+        if (!lse) made_lse = at::empty({g.B, g.H, g.Npad}, on(dev, at::kFloat));
+        if (!ws) made_ws = at::empty({static_cast<long long>(fvattn_attn_workspace_size(&g))}, on(dev, at::kByte));
+        const Tensor* w = ws ? ws : &made_ws;
+        rc = fvattn_sparse_attn_lse(&g, q->data_ptr(), k->data_ptr(), v->data_ptr(), ptr<int32_t>(idx), ptr<int32_t>(cnt),
+                                    scale, out ? out->data_ptr() : made_out.data_ptr(),
+                                    ptr<float>(lse ? lse : &made_lse), nullptr, w->data_ptr(),
+                                    static_cast<size_t>(w->numel()), stream_of(dev));
+    }
+    if (rc != FVATTN_OK) return not_here();
     return pair(given(a[7], std::move(made_out)), given(a[8], std::move(made_lse)));
     END_HANDLE_TH_ERRORS
 }
@@ -293,14 +317,18 @@ PyObject* sparse_attn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         (ws && !dense(ws, dev, at::kByte, {ws->numel()})))
         return not_here();
     Tensor d[3], made_ws;
-    for (Tensor& t : d) t = at::empty({g.B, g.H, g.Npad, g.D}, on(dev, at::kBFloat16));
-    if (!ws) made_ws = at::empty({static_cast<long long>(fvattn_sparse_attn_bwd_workspace_size(&g))}, on(dev, at::kByte));
-    const Tensor* w = ws ? ws : &made_ws;
-    if (fvattn_sparse_attn_bwd(&g, q->data_ptr(), k->data_ptr(), v->data_ptr(), o->data_ptr(), dout->data_ptr(),
-                               ptr<float>(lse), ptr<int32_t>(idx), ptr<int32_t>(cnt), scale, d[0].data_ptr(),
-                               d[1].data_ptr(), d[2].data_ptr(), w->data_ptr(), static_cast<size_t>(w->numel()),
-                               stream_of(dev)) != FVATTN_OK)
-        return not_here();
+    int rc;
+    {
+        Unlocked unlocked;
+        for (Tensor& t : d) t = at::empty({g.B, g.H, g.Npad, g.D}, on(dev, at::kBFloat16));
+        if (!ws) made_ws = at::empty({static_cast<long long>(fvattn_sparse_attn_bwd_workspace_size(&g))}, on(dev, at::kByte));
+        const Tensor* w = ws ? ws : &made_ws;
+        rc = fvattn_sparse_attn_bwd(&g, q->data_ptr(), k->data_ptr(), v->data_ptr(), o->data_ptr(), dout->data_ptr(),
+                                    ptr<float>(lse), ptr<int32_t>(idx), ptr<int32_t>(cnt), scale, d[0].data_ptr(),
+                                    d[1].data_ptr(), d[2].data_ptr(), w->data_ptr(), static_cast<size_t>(w->numel()),
+                                    stream_of(dev));
+    }
+    if (rc != FVATTN_OK) return not_here();
     PyObject *x = THPVariable_Wrap(std::move(d[0])), *y = THPVariable_Wrap(std::move(d[1])), *z = THPVariable_Wrap(std::move(d[2]));
     PyObject* t = x && y && z ? PyTuple_Pack(3, x, y, z) : nullptr;
     Py_XDECREF(x);

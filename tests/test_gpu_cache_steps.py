@@ -444,3 +444,41 @@ def test_rows_that_take_no_part_are_zero_in_queries_made_by_the_call(fv, ca, str
     part = torch.tensor([i in (2, 3, 4, 6) for i in range(rows)], device="cuda")
     assert torch.equal(bits(got[part]), bits(out[part]))
     assert (got[~part] == 0).all() and (out[~part] == 7.0).all()
+
+
+@pytest.mark.parametrize("way", ["extension", "bindings"])
+def test_other_threads_run_while_a_call_waits_for_the_launch_queue(fv, ca, way):  # noqa: F811
+    """A caller that runs ahead fills the stream's launch queue and waits in its next call until the GPU is through
+    the work in front (half a second here); another Python thread goes on meanwhile."""
+    import threading
+    import time
+    c, table, ln = pool(ca, [40, 7], 2, 64, 16, 3)
+    k, v = normal((2, 2, 64), 1), normal((2, 2, 64), 2)
+    here = torch.cuda.current_stream() if way == "bindings" else None
+    c.append(k, v, table, ln, stream=here)
+    torch.cuda.synchronize()
+    stop, gaps = threading.Event(), []
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+
+    other = threading.Thread(target=tick)
+    other.start()
+    start = time.perf_counter()
+    try:
+        torch.cuda._sleep(1_000_000_000)         # clocks: over half a second at most 1965 MHz
+        for _ in range(4000):                    # more launches than a queue holds (1024)
+            c.append(k, v, table, ln, stream=here)
+        ahead = time.perf_counter() - start
+        torch.cuda.synchronize()
+    finally:
+        stop.set()
+        other.join()
+    assert ahead > 0.3                           # the calls did wait
+    assert max(gaps) < 0.15
+    assert fv.get_status() == 0
