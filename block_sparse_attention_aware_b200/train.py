@@ -17,7 +17,7 @@ from typing import Optional
 
 import torch
 
-from . import fvattn
+from . import build, fvattn
 from .fvattn import Geom, _check, _raster
 
 EXPORTED = ("fvattn_sparse_attn_lse", "fvattn_sparse_attn_bwd_workspace_size", "fvattn_sparse_attn_bwd")
@@ -28,10 +28,17 @@ _fast = None      # the extension that serves a call's plain case (csrc/binding.
 
 def native():
     """The extension over the C ABI, which checks and marshals a plain call in
-    2 us and answers NotImplemented to any other (raises if missing)."""
+    2 us and answers NotImplemented to any other (raises if it is missing or
+    was built for another torch)."""
     global _fast
     if _fast is None:
-        from . import _native
+        remedy = "run `python -m block_sparse_attention_aware_b200.build`"
+        try:
+            from . import _native
+        except ImportError as e:
+            raise ImportError(f"_native.so is not built for this torch: {remedy}") from e
+        if _native.target != build.native_target():
+            raise ImportError(f"_native.so was built for {_native.target}, this is {build.native_target()}: {remedy}")
         _fast = _native
     return _fast
 

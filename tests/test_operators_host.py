@@ -344,3 +344,34 @@ def test_failed_calls_leave_no_error_behind(mods, tmp_path):
     done = subprocess.run([sys.executable, "-S", "-c", CALLER, str(lib), fvattn.LIB_PATH], capture_output=True, text=True, timeout=120,
                           env=dict(os.environ, LD_LIBRARY_PATH=str(tmp_path)))
     assert done.returncode == 0 and "done" in done.stdout, done.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ the extension's build
+
+def test_the_extension_is_built_again_for_another_torch(mods, tmp_path, monkeypatch):
+    """Only the extension: the library does not know torch.  Nothing is built where nothing changed."""
+    from block_sparse_attention_aware_b200 import build
+    commands = []
+    monkeypatch.setattr(build.subprocess, "check_call", lambda cmd, *a, **k: commands.append(cmd))
+    monkeypatch.setattr(build.subprocess, "Popen", lambda cmd, *a, **k: pytest.fail("the library is built again"))
+    monkeypatch.setattr(build.os, "replace", lambda a, b: None)
+    build.build()
+    assert commands == []
+    stamp = tmp_path / "native.txt"
+    monkeypatch.setattr(build, "STAMP", str(stamp))
+    stamp.write_text("torch 1.0, Python 3.12")
+    build.build()
+    assert len(commands) == 1 and commands[0][0] == "g++" and stamp.read_text() == build.native_target()
+    build.build()
+    assert len(commands) == 1
+
+
+def test_an_extension_for_another_torch_is_refused(mods, monkeypatch):
+    import types
+    import block_sparse_attention_aware_b200 as package
+    tr = mods[1]
+    assert tr.native().target == tr.build.native_target()
+    monkeypatch.setattr(tr, "_fast", None)
+    monkeypatch.setattr(package, "_native", types.SimpleNamespace(target="torch 1.0, Python 3.12"))
+    with pytest.raises(ImportError, match="built for torch 1.0"):
+        tr.native()
