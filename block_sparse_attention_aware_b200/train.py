@@ -240,7 +240,9 @@ class _Attention(torch.autograd.Function):
         g = ctx.g
         qt, kt, vt, ot, lse, kv_idx, kv_cnt = ctx.saved_tensors
         with torch.cuda.device(qt.device):
-            dot = fvattn.reorder(g, do.contiguous())
+            do = do.contiguous()
+            # a view may start anywhere (the gradient of a concatenation's part), the kernels read 16 bytes at a time
+            dot = fvattn.reorder(g, do if do.data_ptr() % 16 == 0 else do.clone())
             grads = sparse_attn_bwd(g, qt, kt, vt, ot, dot, lse, kv_idx, kv_cnt, ctx.scale)
             dq, dk, dv = (fvattn.inverse_reorder(g, t) if need else None
                           for t, need in zip(grads, ctx.needs_input_grad))

@@ -544,3 +544,18 @@ def test_nan_scores_are_not_taken_for_an_empty_row(fv, tr, keep):  # noqa: F811
             assert l[0, 0, nan].isnan().all() and torch.equal(l[0, 0, ~nan], lse[0, 0, ~nan])
             assert (got[rows // g.bs == 5] == 0).all()
     assert fv.get_status() == 0
+
+
+def test_a_gradient_that_starts_between_16_byte_boundaries(fv, tr):  # noqa: F811
+    """Autograd hands over views: the gradient of a concatenation's part starts wherever that part does."""
+    g = fv.geom(*GEO64)
+    idx, cnt = random_lists(g, 0.5, 6)
+    q, k, v, do = raster(g, 7)
+    leaves = [t.requires_grad_() for t in (q, k, v)]
+    want = torch.autograd.grad(tr.attention(g, *leaves, idx, cnt), leaves, do)
+    o = tr.attention(g, *leaves, idx, cnt)
+    joined = torch.cat([torch.zeros(3, dtype=BF16, device="cuda"), o.flatten()])
+    got = torch.autograd.grad(joined, leaves, torch.cat([torch.zeros(3, dtype=BF16, device="cuda"), do.flatten()]))
+    for a, b in zip(got, want):
+        assert torch.equal(bits(a), bits(b))
+    assert fv.get_status() == 0
