@@ -259,8 +259,8 @@ def attention(g: Geom, q, k, v, kv_idx, kv_cnt, scale: Optional[float] = None, o
         _need(name, t, _raster(g), torch.bfloat16, dev)
     _need("kv_idx", kv_idx, (g.B, g.H, g.nb, g.nb), torch.int32, dev)
     _need("kv_cnt", kv_cnt, (g.B, g.H, g.nb), torch.int32, dev)
-    if g.order and order is None:
-        raise ValueError("a geometry with a block order needs its table: pass order=")
+    if g.order and (order is None or order.data_ptr() != g.order):
+        raise ValueError("order: a geometry with a block order needs the table that it was made with")
     return _Attention.apply(q, k, v, g, order, None, kv_idx, kv_cnt, scale)
 
 

@@ -559,3 +559,16 @@ def test_a_gradient_that_starts_between_16_byte_boundaries(fv, tr):  # noqa: F81
     for a, b in zip(got, want):
         assert torch.equal(bits(a), bits(b))
     assert fv.get_status() == 0
+
+
+def test_attention_takes_its_own_geometrys_order_only(fv, tr):  # noqa: F811
+    g = fv.geom(*GEO)
+    idx, cnt = random_lists(g, 0.5, 6)
+    q, k, v, _ = raster(g, 7)
+    mine, other = fv.block_order(g), fv.block_order(g)
+    ordered = fv.with_order(g, mine)
+    assert torch.equal(bits(tr.attention(ordered, q, k, v, idx, cnt, order=mine)), bits(tr.attention(
+        fv.with_order(g, other), q, k, v, idx, cnt, order=other)))
+    for geo, table in ((ordered, other), (ordered, None)):
+        with pytest.raises(ValueError, match="order"):
+            tr.attention(geo, q, k, v, idx, cnt, order=table)
