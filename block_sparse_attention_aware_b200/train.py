@@ -261,6 +261,8 @@ def attention(g: Geom, q, k, v, kv_idx, kv_cnt, scale: Optional[float] = None, o
     _need("kv_cnt", kv_cnt, (g.B, g.H, g.nb), torch.int32, dev)
     if g.order and (order is None or order.data_ptr() != g.order):
         raise ValueError("order: a geometry with a block order needs the table that it was made with")
+    if g.order and order.device != dev:
+        raise ValueError(f"order: expected on {dev}, got {order.device}")
     return _Attention.apply(q, k, v, g, order, None, kv_idx, kv_cnt, scale)
 
 
@@ -289,6 +291,8 @@ class TrainLayer:
         dev = _device("q", q)
         for name, t in (("q", q), ("k", k), ("v", v)):
             _need(name, t, _raster(self.g), torch.bfloat16, dev)
+        if self.order_table is not None and self.order_table.device != dev:
+            raise ValueError(f"q: on {dev}, the layer's block order is on {self.order_table.device}")
         with torch.cuda.device(q.device):
             qt, kt, routed = self.route(q, k)
         return _Attention.apply(q, k, v, self.g, self.order_table, (qt, kt), routed.kv_idx, routed.kv_cnt, self.scale)

@@ -572,3 +572,15 @@ def test_attention_takes_its_own_geometrys_order_only(fv, tr):  # noqa: F811
     for geo, table in ((ordered, other), (ordered, None)):
         with pytest.raises(ValueError, match="order"):
             tr.attention(geo, q, k, v, idx, cnt, order=table)
+
+
+def test_a_layers_block_order_is_on_its_tensors_device(fv, tr):  # noqa: F811
+    """A table elsewhere would be read through an address that this GPU does not have: refused before any launch."""
+    g = fv.geom(*GEO)
+    q, k, v, _ = raster(g, 7)
+    layer = tr.TrainLayer(g, 0.9, 2, order="hilbert")
+    layer(q, k, v)
+    layer.order_table = layer.order_table.cpu()
+    with pytest.raises(ValueError, match="order"):
+        layer(q, k, v)
+    assert fv.get_status() == 0
