@@ -82,11 +82,14 @@ int fvattn_cache_append_fresh(const fvattn_cache *c, int B, long long rows, cons
 
 /* Parts that fvattn_cache_attn splits a sequence's tokens into, for up to
  * `longest` tokens a sequence, and the tokens a part holds (a multiple of
- * 64).  They follow from the arguments alone.  0 for bad arguments. */
+ * 64).  They follow from the arguments and the number of SMs of the current
+ * device (148 without one).  0 for bad arguments. */
 int fvattn_cache_attn_parts(int B, int Hq, int Hkv, int D, long long longest, int *tokens);
 
 /* Bytes of device workspace fvattn_cache_attn needs (0 when it does not
- * split): per query head and part D + 2 fp32. */
+ * split): per query head and part D + 2 fp32.  Asked for with the call's
+ * device current: another GPU may split otherwise, and a workspace sized for
+ * it be refused. */
 size_t fvattn_cache_attn_workspace_size(int B, int Hq, int Hkv, int D, long long longest);
 
 /* Attention of one query a sequence over its cached tokens: for each head j
