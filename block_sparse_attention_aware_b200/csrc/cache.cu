@@ -4,7 +4,7 @@
 // Append moves every new key, value and query once: a bit copy of V and
 // (a, b) -> (a c - b s, a s + b c) on the pairs of K and Q, bound by memory.
 // One CTA a token, eight CTAs an SM: two frames of 1560 tokens with 40 query
-// and 40 key heads of 128 take 35.8 us, 5.4 TB/s read and written.  (Loads for
+// and 40 key heads of 128 take 35.9 us, 5.4 TB/s read and written.  (Loads for
 // four heads in flight a thread cost CTAs an SM, and 42 us; four tokens a CTA
 // likewise, 41 to 49.)  A single token takes 2.5 us.
 //

@@ -57,7 +57,7 @@
 // each row sees only the columns of blocks that its own block is paired with.
 //
 // What bounds it.  A 720p layer (40 heads, 13.8 million pairs of 128-token
-// blocks, D = 128) takes 321 to 328 ms by the board: 902 TFLOP/s counted as five products,
+// blocks, D = 128) takes 321 to 330 ms by the board: 902 TFLOP/s counted as five products,
 // 1264 as the seven that run, 92% of what a large matrix product sustains under the
 // board's power limit (1368); the clock settles at 1.7 GHz and falls when the
 // pipe is kept busier, so a form with 10% fewer clocks a chunk (P and dS both
@@ -66,7 +66,7 @@
 // common body, two issuers 9.0 (with the exact delta's product); that product
 // where it is needed only, dP double buffered 7.75; four warpgroups of
 // arithmetic instead of two 7.7 (blocks of 64: 1.31 to 1.10 ms); issuers from
-// uniform registers 7.1 to 7.4 (by the board).  Rows that see none of a chunk's
+// uniform registers 7.1 to 7.5 (by the board).  Rows that see none of a chunk's
 // columns skip its arithmetic: 344 to 275 us for lists of 5% of 448 blocks of 32.
 #include <cuda.h>
 
